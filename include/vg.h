@@ -18,6 +18,11 @@
  *   vg_iteration          verify -> select -> gamma draft steps, in stream order.
  *   vg_iteration_plan_*   the same iteration captured once as a CUDA graph and
  *                         launched step after step.
+ * Around a batch of such sequences:
+ *   vg_rope_append        rotary positions of new q and k rows; k and v enter the cache;
+ *   vg_pages_resize, vg_pages_fork, vg_pages_compact
+ *                         the page pool behind a block table: rows grown, cut and freed,
+ *                         branches that share a parent's pages, live pages moved together.
  *
  * Conventions shared by every call
  *   - All tensor arguments are DEVICE pointers to caller-owned memory, unless a
@@ -71,6 +76,7 @@ typedef int32_t vg_status;
 #define VG_ERR_CUDA (-4)               /* a CUDA runtime call failed                 */
 #define VG_ERR_DEVICE_TIMEOUT (-5)     /* device: a bounded wait ran out             */
 #define VG_ERR_DEVICE_BOUNDS (-6)      /* device: length or index out of range       */
+#define VG_ERR_DEVICE_PAGES (-7)       /* device: the page pool has too few free pages */
 
 /* Problem dimensions (host struct). */
 typedef struct vg_dims {
@@ -332,8 +338,144 @@ vg_status vg_accept(int32_t B, int32_t gamma, int32_t V, const float* p_logits, 
                     uint32_t mode, int32_t* n_accept, int32_t* next_token, int32_t* advance_len,
                     void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
-/* Bytes of workspace any call above needs for these dimensions on the current
- * device (0 on invalid dims or no device; see vg_last_error()). */
+/*
+ * Rotary positions of new q and k rows, and the append of k and v to the cache.  No
+ * counterpart in the page, whose engine rotates inside the model; it is the step before
+ * vg_verify_attn (which then takes k_new = v_new = NULL) and before a prompt's attention.
+ *
+ * Row r of the packed rows belongs to sequence b at position pos = prefix_len[b] + t, t its
+ * index among b's rows.  In every q and k head each pair (x, y) of the first rot_dim
+ * elements becomes (x c - y s, x s + y c), c and s being mscale times the cosine and sine of
+ * pos * f_i; the elements from rot_dim on are copied.  q goes to q_out, k and v (as it is)
+ * to the cache slot of position pos.
+ *
+ *   rope->freq     device uint64 [rot_dim / 2]: f_i as a fraction of a turn per position,
+ *                  round(f_i / 2pi * 2^64) (vg_rope_freqs fills a host array).  The angle is
+ *                  exact to pos * 2^-65 of a turn at any position.
+ *   rope->rot_dim  even, 2 .. d.   rope->layout  VG_ROPE_HALF: pairs (i, i + rot_dim / 2);
+ *                  VG_ROPE_INTERLEAVED: pairs (2i, 2i + 1).
+ *   rope->mscale   finite; 0 means 1.
+ *   q, k, v, q_out bf16 [n_rows][H_q or H_kv][d] with row strides in elements (multiples of
+ *                  8, at least heads * d), so that the three may be slices of one projection's
+ *                  output.  q_out may be q itself with the same stride; else it overlaps
+ *                  none of the inputs, and no input overlaps the cache.
+ *   row_start      device int32 [B + 1], ascending from 0: b's rows are row_start[b] ..
+ *                  row_start[b + 1] - 1 (none, if equal).  Rows from row_start[B] on, up to
+ *                  n_rows, are padding: nothing is read or written for them.  NULL: every
+ *                  sequence has gamma + 1 rows, and n_rows must be B * (gamma + 1).
+ *   prefix_len     device int32 [B], each in [0, max_len]: tokens in the cache before the rows.
+ * A row whose prefix length is out of range is left alone, one whose slot lies outside the
+ * cache is not appended (its q is still rotated); both report VG_ERR_DEVICE_BOUNDS.  Any
+ * page_size >= 1.  n_rows in [0, 2^24]; uses no workspace; one launch (none for 0 rows).
+ */
+#define VG_ROPE_HALF 0
+#define VG_ROPE_INTERLEAVED 1
+typedef struct vg_rope {
+  const uint64_t* freq;
+  int32_t rot_dim;
+  int32_t layout;
+  float mscale;
+} vg_rope;
+vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg_rope* rope, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* row_start, int32_t n_rows, const int32_t* prefix_len, void* q_out,
+                         int64_t q_out_stride, int32_t* dev_status, void* stream);
+
+/*
+ * The frequencies of vg_rope_append, computed on the host in 64 bits into freq (HOST memory,
+ * rot_dim / 2 entries; the caller copies them to the device).  f_i = base^(-2i / rot_dim), then
+ *   VG_ROPE_PLAIN   as it is;
+ *   VG_ROPE_LINEAR  f_i / factor (positions compressed by factor);
+ *   VG_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) instead of base (rot_dim > 2), which
+ *                   leaves the fastest pair and divides the slowest by factor;
+ *   VG_ROPE_RAMP    by parts: a pair that turns r = orig_len * f_i / 2pi times within the
+ *                   original context keeps f_i if r >= fast, gets f_i / factor if r <= slow, and
+ *                   a blend linear in r between.  (A common choice of mscale beside it is
+ *                   0.1 ln(factor) + 1.)
+ * base > 0, factor > 0 (finite), every resulting f_i below 2pi; RAMP: orig_len > 0 and
+ * 0 <= slow < fast.  Arguments that a kind does not name are ignored.  No device needed.
+ */
+#define VG_ROPE_PLAIN 0u
+#define VG_ROPE_LINEAR 1u
+#define VG_ROPE_BASE 2u
+#define VG_ROPE_RAMP 3u
+vg_status vg_rope_freqs(int32_t rot_dim, double base, uint32_t scaling, double factor, double orig_len, double slow,
+                        double fast, uint64_t* freq);
+
+/*
+ * The page pool behind a block table (vg_kv_cache.page_table), kept on the device and
+ * changed there, so that a decode loop never waits for the host.  No counterpart in the
+ * page, whose engine manages its pages itself.  A host struct of device pointers:
+ *   page_table  int32 [n_seqs][pages_per_seq], as vg_kv_cache reads it (the first rows of a
+ *               table of n_seqs rows serve a batch of B <= n_seqs sequences);
+ *   held        int32 [n_seqs]: row s holds its first held[s] entries; later ones are not read;
+ *   refs        int32 [n_pages]: how often a page is held, 0 (or less): free.
+ * One table serves every layer: page p of a layer is its slots p * page_size and on.  A new
+ * pool is held = 0 and refs = 0; a page that must never be handed out keeps refs > 0.
+ * page_size in [1, 2^20], n_pages * page_size < 2^31, n_seqs <= 65536,
+ * n_seqs * pages_per_seq < 2^31.
+ *
+ * Requests are served in order, all releases before any page is handed out, the lowest free
+ * pages first: the result depends on the state and the request alone.  Reported on the
+ * device, the request then changing nothing: VG_ERR_DEVICE_BOUNDS for a row outside the table
+ * or named twice (the first one counts), a length that does not fit pages_per_seq pages (or is
+ * negative, or longer than what the parent holds).  VG_ERR_DEVICE_PAGES: the pool ran out; the
+ * request keeps what it had after releases, and so do all later ones that need pages.  Calls
+ * that share a pool or a workspace must be ordered on one stream.
+ * Workspace: vg_pages_workspace_size bytes (0 on a bad pool), 256-byte aligned, contents
+ * arbitrary before and after.  All pointers 16-byte aligned.
+ */
+typedef struct vg_page_pool {
+  int32_t* page_table;
+  int32_t* held;
+  int32_t* refs;
+  int32_t n_seqs;
+  int32_t pages_per_seq;
+  int32_t n_pages;
+  int32_t page_size;
+} vg_page_pool;
+size_t vg_pages_workspace_size(const vg_page_pool* pool);
+
+/*
+ * Rows grown, cut or freed: row seq[j] holds ceil(length[j] / page_size) pages afterwards
+ * (j < n; length 0 frees it).  Pages past that are given back (their entries become -1);
+ * missing ones are appended.  Cutting a row inside a page that other rows hold leaves that
+ * page shared: fork the row before tokens are appended there.
+ *   seq  device int32 [n], or NULL for rows 0 .. n-1;  length  device int32 [n];  0 <= n <= n_seqs
+ */
+vg_status vg_pages_resize(const vg_page_pool* pool, const int32_t* seq, const int32_t* length, int32_t n, void* ws,
+                          size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Branches: row child[j] becomes a copy of the first length[j] tokens of row parent[j], with
+ * room for `room` more.  What the child held is given back; whole pages are shared (their
+ * references counted); the page that length[j] ends inside is copied, the tokens in use only,
+ * in every layer, so that both rows may append; ceil((length + room) / page_size) pages are
+ * held.  A row may be the parent of many, but not parent and child in one call.  If the pool
+ * runs out, the child holds nothing.
+ *   caches  host array of n_layers caches (1 .. 128): K, V and capacity_slots are read, each
+ *           with at least n_pages * page_size slots;  token_bytes  bytes of one slot of K
+ *           (H_kv * d * 2), a multiple of 16, up to 2^20
+ *   parent, child, length  device int32 [n], 0 <= n <= n_seqs;  room >= 0
+ */
+vg_status vg_pages_fork(const vg_page_pool* pool, const vg_kv_cache* caches, int32_t n_layers, int32_t token_bytes,
+                        const int32_t* parent, const int32_t* child, const int32_t* length, int32_t n, int32_t room,
+                        void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Holes closed: with n_live pages in use, the ones from index n_live on move into the free
+ * ones below it (ascending into ascending), contents of every layer included; afterwards
+ * pages 0 .. n_live - 1 are in use.  Entries of the rows that held a moved page name its new
+ * place in page_table_out, and its references are in refs_out; both may be the pool's own
+ * arrays (in place) or must not overlap them.  Entries past held are copied as they are.
+ * Moved pages' old contents stay where they were.  n_live: device int32 (the count).
+ */
+vg_status vg_pages_compact(const vg_page_pool* pool, const vg_kv_cache* caches, int32_t n_layers, int32_t token_bytes,
+                           int32_t* page_table_out, int32_t* refs_out, int32_t* n_live, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
+/* Bytes of workspace any call of an iteration (verify, select, draft) needs for these
+ * dimensions on the current device (0 on invalid dims or no device; see vg_last_error()). */
 size_t vg_workspace_size(const vg_dims* dims, int32_t k);
 
 /* Kernels one vg_sparse_draft_attn call with these dimensions enqueues on the current

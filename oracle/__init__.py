@@ -29,3 +29,8 @@ from .vegas import (  # noqa: F401
     next_prefix_len,
     paged_slots,
 )
+from .batch import (  # noqa: F401
+    Pool,
+    rope,
+    rope_inverse,
+)

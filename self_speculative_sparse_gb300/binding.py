@@ -21,11 +21,14 @@ VG_ERR_WORKSPACE = -3
 VG_ERR_CUDA = -4
 VG_ERR_DEVICE_TIMEOUT = -5
 VG_ERR_DEVICE_BOUNDS = -6
+VG_ERR_DEVICE_PAGES = -7
 
 ENTRY_POINTS = ("vg_verify_attn", "vg_topk_select", "vg_window_select", "vg_sparse_draft_attn", "vg_iteration",
                 "vg_iteration_plan_create", "vg_iteration_plan_launch", "vg_iteration_plan_destroy",
                 "vg_sparse_draft_attn_noalloc", "vg_workspace_size", "vg_sparse_draft_launches",
                 "vg_accept", "vg_accept_workspace_size",
+                "vg_rope_append", "vg_rope_freqs", "vg_pages_resize", "vg_pages_fork", "vg_pages_compact",
+                "vg_pages_workspace_size",
                 "vg_last_error", "vg_version", "vg_selftest_lost_wait")
 
 
@@ -57,6 +60,17 @@ class vg_iter_outputs(ctypes.Structure):
     _fields_ = [("out_verify", ctypes.c_void_p), ("scores0", ctypes.c_void_p), ("scores1", ctypes.c_void_p),
                 ("score_stride", ctypes.c_int64), ("idx", ctypes.c_void_p), ("count", ctypes.c_void_p),
                 ("idx1", ctypes.c_void_p), ("count1", ctypes.c_void_p), ("out_draft", ctypes.c_void_p)]
+
+
+class vg_rope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class vg_page_pool(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 _lib = None
@@ -104,6 +118,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.vg_accept.restype = i32
     L.vg_sparse_draft_launches.argtypes = [ctypes.POINTER(vg_dims), i32, i32]
     L.vg_sparse_draft_launches.restype = i32
+    f64 = ctypes.c_double
+    L.vg_rope_append.argtypes = [ctypes.POINTER(vg_dims), ctypes.POINTER(vg_kv_cache), ctypes.POINTER(vg_rope), vp, i64,
+                                 vp, i64, vp, i64, vp, i32, vp, vp, i64, vp, vp]
+    L.vg_rope_append.restype = i32
+    L.vg_rope_freqs.argtypes = [i32, f64, u32, f64, f64, f64, f64, vp]
+    L.vg_rope_freqs.restype = i32
+    L.vg_pages_workspace_size.argtypes = [ctypes.POINTER(vg_page_pool)]
+    L.vg_pages_workspace_size.restype = sz
+    L.vg_pages_resize.argtypes = [ctypes.POINTER(vg_page_pool), vp, vp, i32, vp, sz, vp, vp]
+    L.vg_pages_resize.restype = i32
+    L.vg_pages_fork.argtypes = [ctypes.POINTER(vg_page_pool), ctypes.POINTER(vg_kv_cache), i32, i32, vp, vp, vp, i32,
+                                i32, vp, sz, vp, vp]
+    L.vg_pages_fork.restype = i32
+    L.vg_pages_compact.argtypes = [ctypes.POINTER(vg_page_pool), ctypes.POINTER(vg_kv_cache), i32, i32, vp, vp, vp, vp,
+                                   sz, vp, vp]
+    L.vg_pages_compact.restype = i32
     L.vg_last_error.argtypes = []
     L.vg_last_error.restype = ctypes.c_char_p
     L.vg_version.argtypes = []
@@ -248,6 +278,79 @@ def vg_sparse_draft_attn_noalloc(dims, cache, q, k_new, v_new, idx, count, k_str
     _check(load().vg_sparse_draft_attn_noalloc(ctypes.byref(dims), ctypes.byref(cache), ptr(q), ptr(k_new),
                                                ptr(v_new), ptr(idx), ptr(count), k_stride, ptr(tail_start),
                                                ptr(tail_len), ptr(out), ptr(dev_status), _stream(stream)))
+
+
+VG_ROPE_HALF = 0
+VG_ROPE_INTERLEAVED = 1
+VG_ROPE_PLAIN = 0
+VG_ROPE_LINEAR = 1
+VG_ROPE_BASE = 2
+VG_ROPE_RAMP = 3
+
+
+def vg_rope_freqs(rot_dim: int, base: float, scaling: int = VG_ROPE_PLAIN, factor: float = 1.0,
+                  orig_len: float = 0.0, slow: float = 1.0, fast: float = 32.0):
+    """The frequencies of vg_rope_append as a numpy uint64 array [rot_dim / 2] (host); copy it
+    to the device, e.g. ``torch.from_numpy(a.view("int64")).cuda()``."""
+    import numpy as np
+    out = np.empty(max(rot_dim, 2) // 2, dtype=np.uint64)
+    _check(load().vg_rope_freqs(rot_dim, base, scaling, factor, orig_len, slow, fast, out.ctypes.data))
+    return out
+
+
+def make_rope(freq, rot_dim: int, layout: int = VG_ROPE_HALF, mscale: float = 0.0) -> vg_rope:
+    """The rotation of vg_rope_append; freq: the frequencies on the device (64-bit integers)."""
+    return vg_rope(ptr(freq), rot_dim, layout, mscale)
+
+
+def vg_rope_append(dims, cache, rope: vg_rope, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows, prefix_len,
+                   q_out, q_out_stride, dev_status=None, stream=None) -> None:
+    """Rotate q and k rows at their positions; q to q_out, k and v into the cache."""
+    _check(load().vg_rope_append(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(rope), ptr(q), q_stride, ptr(k),
+                                 k_stride, ptr(v), v_stride, ptr(row_start), n_rows, ptr(prefix_len), ptr(q_out),
+                                 q_out_stride, ptr(dev_status), _stream(stream)))
+
+
+def make_pages(page_table, held, refs, page_size: int) -> vg_page_pool:
+    """The page pool of int32 tensors page_table [n_seqs][pages_per_seq], held [n_seqs], refs [n_pages]."""
+    return vg_page_pool(ptr(page_table), ptr(held), ptr(refs), page_table.shape[0], page_table.shape[1],
+                        refs.shape[0], page_size)
+
+
+def make_caches(layers):
+    """The host array of cache structs that the page calls take, from (K, V) tensors of each
+    layer ([capacity_slots][...])."""
+    return (vg_kv_cache * len(layers))(*[make_cache(K, V, None) for K, V in layers])
+
+
+def vg_pages_workspace_size(pool: vg_page_pool) -> int:
+    n = load().vg_pages_workspace_size(ctypes.byref(pool))
+    if n == 0:
+        raise VgError(VG_ERR_INVALID_ARG, load().vg_last_error().decode())
+    return n
+
+
+def vg_pages_resize(pool: vg_page_pool, seq, length, n, ws, ws_bytes=None, dev_status=None, stream=None) -> None:
+    """Grow, cut or free rows to hold length[j] tokens each."""
+    wsb = ws_bytes if ws_bytes is not None else (ws.numel() * ws.element_size() if ws is not None else 0)
+    _check(load().vg_pages_resize(ctypes.byref(pool), ptr(seq), ptr(length), n, ptr(ws), wsb, ptr(dev_status),
+                                  _stream(stream)))
+
+
+def vg_pages_fork(pool: vg_page_pool, caches, token_bytes, parent, child, length, n, room, ws, ws_bytes=None,
+                  dev_status=None, stream=None) -> None:
+    """Rows child[j] become branches of the first length[j] tokens of rows parent[j]."""
+    wsb = ws_bytes if ws_bytes is not None else (ws.numel() * ws.element_size() if ws is not None else 0)
+    _check(load().vg_pages_fork(ctypes.byref(pool), caches, len(caches), token_bytes, ptr(parent), ptr(child),
+                                ptr(length), n, room, ptr(ws), wsb, ptr(dev_status), _stream(stream)))
+
+
+def vg_pages_compact(pool: vg_page_pool, caches, token_bytes, page_table_out, refs_out, n_live, ws, ws_bytes=None,
+                     dev_status=None, stream=None) -> None:
+    """Move the live pages to the front of the pool, contents of every layer included."""
+    wsb = ws_bytes if ws_bytes is not None else (ws.numel() * ws.element_size() if ws is not None else 0)
+    _check(load().vg_pages_compact(ctypes.byref(pool), caches, len(caches), token_bytes, ptr(page_table_out),
+                                   ptr(refs_out), ptr(n_live), ptr(ws), wsb, ptr(dev_status), _stream(stream)))
 
 
 def vg_selftest_lost_wait(limit_us, dev_status, elapsed_ns=None, stream=None) -> None:

@@ -1,0 +1,418 @@
+// The page pool of a paged cache: rows of the block table grown, cut, forked and freed, and
+// live pages moved down to the front of the pool.
+//
+// The state is three integer arrays on the device: the block table, the pages each row
+// holds, and a reference count per page (0: free).  A request never waits for the host:
+// one cluster of CTAs gives pages back, counts what is free, and hands out the lowest free
+// pages to the requests in order, so a result depends on the state and the request alone
+// (counts are added to atomically, but sums of integers do not depend on the order).
+// What has to be read is the reference counts (4 bytes a page) and the rows that a request
+// names; the rest is latency: the phases are separated by cluster barriers, and the cluster
+// grows with the pool (one CTA up to kPagesPerCta pages), since a barrier of one CTA is
+// several times cheaper than one of sixteen.
+//
+// Page contents move in a second kernel, launched as a programmatic dependent over all SMs,
+// from a list of (source page, destination page, tokens) that the first one leaves: reads
+// and writes of whole 16-byte vectors, bound by memory.  Sources and destinations are
+// disjoint (destinations were free), so the copies need no order.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "vg_common.cuh"
+#include "vg_internal.h"
+
+namespace vg {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPageThreads = 1024;
+constexpr int kPageMaxCluster = 16;
+constexpr int kPagesPerCta = 8192;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBytes = 16384;  // bytes of one copy item
+
+// Exclusive scan over the CTA's threads; *total gets the sum.  All threads.
+__device__ __forceinline__ int block_scan(int v, int* sh, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = lane < kPageThreads / 32 ? sh[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += t;
+    }
+    sh[lane] = y;
+  }
+  __syncthreads();
+  const int base = warp > 0 ? sh[warp - 1] : 0;
+  *total = sh[kPageThreads / 32 - 1];
+  __syncthreads();
+  return base + x - v;
+}
+
+// This thread's contiguous run of pages [lo, hi): the pool is cut into equal runs, a
+// multiple of four pages each.
+__device__ __forceinline__ void page_run(int n_pages, int rank, int nctas, int& lo, int& hi) {
+  const int threads = nctas * kPageThreads;
+  const int per = ((n_pages + threads - 1) / threads + 3) & ~3;
+  const int64_t at = static_cast<int64_t>(rank * kPageThreads + threadIdx.x) * per;
+  lo = static_cast<int>(at < n_pages ? at : n_pages);
+  hi = static_cast<int>(at + per < n_pages ? at + per : n_pages);
+}
+
+// Pages of the run that are free (other CTAs' counts come through L2).
+__device__ __forceinline__ int count_free(const int32_t* refs, int lo, int hi) {
+  int n = 0;
+  int i = lo;
+  for (; i + 4 <= hi; i += 4) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(refs + i));
+    n += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
+  }
+  for (; i < hi; ++i) n += __ldcg(refs + i) <= 0;
+  return n;
+}
+
+struct ClusterShared {
+  int sh[32];
+  int counts[kPageMaxCluster];  // every CTA's count, pushed by its owner
+};
+
+// Grow, cut or fork rows (one cluster).
+__global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const PagesParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
+  __shared__ ClusterShared s;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int gt = rank * kPageThreads + tid, GT = C * kPageThreads;  // thread of the cluster
+  const int gw = gt >> 5, GW = GT >> 5;                             // warp of the cluster
+  pdl_wait();
+  // ---- which request names each row first (a row named twice: the later ones are refused)
+  for (int j = gt; j < p.n; j += GT) {
+    const int c = p.seq ? p.seq[j] : j;
+    if (c >= 0 && c < p.n_seqs) p.owner[c] = INT_MAX;
+    if (p.parent) {
+      const int f = p.parent[j];
+      if (f >= 0 && f < p.n_seqs) p.owner[f] = INT_MAX;
+    }
+  }
+  cluster.sync();
+  for (int j = gt; j < p.n; j += GT) {
+    const int c = p.seq ? p.seq[j] : j;
+    if (c >= 0 && c < p.n_seqs) atomicMin(p.owner + c, j);
+  }
+  cluster.sync();
+  // ---- check each request, give back what its row no longer holds
+  for (int j = gw; j < p.n; j += GW) {
+    const int c = p.seq ? p.seq[j] : j;
+    const int len = p.length[j];
+    bool ok = c >= 0 && c < p.n_seqs && __ldcg(p.owner + c) == j && len >= 0;
+    int total = 0, have = 0, held = 0;
+    if (ok) {
+      held = p.held[c];
+      const int64_t want = (static_cast<int64_t>(len) + p.room + p.page_size - 1) / p.page_size;
+      ok = held >= 0 && held <= p.pages_per_seq && want <= p.pages_per_seq;
+      total = static_cast<int>(want);
+    }
+    if (ok && p.parent) {
+      const int f = p.parent[j];
+      ok = f >= 0 && f < p.n_seqs && __ldcg(p.owner + f) == INT_MAX;
+      if (ok) {
+        const int fh = p.held[f];
+        ok = fh >= 0 && fh <= p.pages_per_seq && len <= static_cast<int64_t>(fh) * p.page_size;
+      }
+    }
+    int keep = 0;
+    if (ok) {
+      if (p.parent) {
+        have = len / p.page_size;  // whole pages shared with the parent
+      } else {
+        have = keep = min(held, total);
+      }
+      int32_t* row = p.table + static_cast<int64_t>(c) * p.pages_per_seq;
+      for (int i = keep + lane; i < held; i += 32) {
+        const int pg = row[i];
+        if (pg >= 0 && pg < p.n_pages) {
+          if (atomicSub(p.refs + pg, 1) <= 0) {  // it was not held: the count goes back
+            atomicAdd(p.refs + pg, 1);
+            report(p.status, VG_ERR_DEVICE_BOUNDS);
+          }
+        } else {
+          report(p.status, VG_ERR_DEVICE_BOUNDS);
+        }
+        row[i] = -1;
+      }
+    } else if (lane == 0) {
+      report(p.status, VG_ERR_DEVICE_BOUNDS);
+    }
+    if (lane == 0) {
+      p.need[j] = ok ? total - have : 0;
+      p.have[j] = ok ? have : -1;
+    }
+  }
+  cluster.sync();
+  // ---- free pages of every CTA's share; each request's rank among the pages handed out
+  int lo, hi, mine, run_free;
+  page_run(p.n_pages, rank, C, lo, hi);
+  run_free = count_free(p.refs, lo, hi);
+  const int before = block_scan(run_free, s.sh, &mine);
+  if (tid < C) *cluster.map_shared_rank(s.counts + rank, tid) = mine;
+  if (rank == C - 1) {
+    const int per = (p.n + kPageThreads - 1) / kPageThreads;
+    const int a = min(tid * per, p.n), b = min(a + per, p.n);
+    int sum = 0, all;
+    for (int j = a; j < b; ++j) sum += __ldcg(p.need + j);
+    int at = block_scan(sum, s.sh, &all);
+    for (int j = a; j < b; ++j) {
+      p.start[j] = at;
+      at += __ldcg(p.need + j);
+    }
+    if (tid == 0) *p.needed = all;
+  }
+  cluster.sync();
+  // ---- the lowest free pages, as many as are asked for
+  int base = before, free_all = 0;
+  for (int c = 0; c < C; ++c) {
+    if (c < rank) base += s.counts[c];
+    free_all += s.counts[c];
+  }
+  const int needed = __ldcg(p.needed);
+  if (base < needed) {
+    for (int i = lo; i < hi && base < needed; ++i)
+      if (__ldcg(p.refs + i) <= 0) p.freelist[base++] = i;
+  }
+  cluster.sync();
+  pdl_launch_dependents();
+  // ---- fill the rows
+  for (int j = gw; j < p.n; j += GW) {
+    const int have = __ldcg(p.have + j);
+    if (p.copies && lane == 0) p.copies[j] = make_int4(0, 0, 0, 0);
+    if (have < 0) continue;
+    const int c = p.seq ? p.seq[j] : j;
+    const int need = __ldcg(p.need + j), start = __ldcg(p.start + j);
+    int32_t* row = p.table + static_cast<int64_t>(c) * p.pages_per_seq;
+    if (need > 0 && start + need > free_all) {  // the pool ran out at an earlier request or here
+      if (lane == 0) {
+        report(p.status, VG_ERR_DEVICE_PAGES);
+        p.held[c] = p.parent ? 0 : have;
+      }
+      continue;
+    }
+    if (p.parent) {
+      const int32_t* from = p.table + static_cast<int64_t>(p.parent[j]) * p.pages_per_seq;
+      for (int i = lane; i < have; i += 32) {
+        const int pg = from[i];
+        row[i] = pg;
+        if (pg >= 0 && pg < p.n_pages)
+          atomicAdd(p.refs + pg, 1);
+        else
+          report(p.status, VG_ERR_DEVICE_BOUNDS);
+      }
+      const int part = p.length[j] % p.page_size;
+      if (lane == 0 && part > 0) {
+        const int src = from[have], dst = __ldcg(p.freelist + start);
+        if (src >= 0 && src < p.n_pages)
+          p.copies[j] = make_int4(src, dst, part, 0);
+        else
+          report(p.status, VG_ERR_DEVICE_BOUNDS);
+      }
+    }
+    for (int i = lane; i < need; i += 32) {
+      const int pg = __ldcg(p.freelist + start + i);
+      row[have + i] = pg;
+      p.refs[pg] = 1;
+    }
+    if (lane == 0) p.held[c] = have + need;
+  }
+}
+
+// Live pages past the count of live pages take the free ones below it, in order.
+__global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const PagesParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
+  __shared__ ClusterShared s;
+  const int tid = threadIdx.x;
+  const int gt = rank * kPageThreads + tid, GT = C * kPageThreads;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  pdl_wait();
+  int lo, hi, mine;
+  page_run(p.n_pages, rank, C, lo, hi);
+  const int run_free = count_free(p.refs, lo, hi);
+  const int before = block_scan(run_free, s.sh, &mine);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory may be written
+  if (tid < C) *cluster.map_shared_rank(s.counts + rank, tid) = mine;
+  cluster.sync();
+  int free_before = before, free_all = 0;  // free pages before this run, in all
+  for (int c = 0; c < C; ++c) {
+    if (c < rank) free_before += s.counts[c];
+    free_all += s.counts[c];
+  }
+  const int n_live = p.n_pages - free_all;
+  // holes (free pages below n_live) in ascending order; movers (live pages from n_live on)
+  // counted from the last one, which needs no count of the holes
+  int f = free_before;
+  for (int i = lo; i < hi; ++i) {
+    const int r = p.refs[i];
+    if (i == n_live) *p.needed = f;  // holes, and so movers
+    if (r <= 0) {
+      if (i < n_live) {
+        p.freelist[f] = i;
+      } else {
+        p.refs_out[i] = 0;
+        p.moved_to[i] = -1;
+      }
+      ++f;
+    } else if (i >= n_live) {
+      p.movers[n_live - 1 - (i - f)] = i;
+    } else {
+      p.refs_out[i] = r;
+    }
+  }
+  if (n_live == p.n_pages && gt == 0) *p.needed = 0;  // (no page at index n_live)
+  if (gt == 0) *p.n_live = n_live;
+  cluster.sync();
+  const int moves = __ldcg(p.needed);
+  pdl_launch_dependents();
+  for (int r = gt; r < moves; r += GT) {
+    const int hole = __ldcg(p.freelist + r), from = __ldcg(p.movers + moves - 1 - r);
+    p.moved_to[from] = hole;
+    const int refs = p.refs[from];
+    p.refs_out[hole] = refs;
+    p.refs_out[from] = 0;
+  }
+}
+
+// One 16 KB piece of a page's tokens.
+__device__ __forceinline__ void copy_piece(const char* src, char* dst, int bytes) {
+  constexpr int U = kCopyBytes / (16 * kCopyThreads);  // vectors a thread
+  uint4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int at = (u * kCopyThreads + threadIdx.x) * 16;
+    if (at < bytes) v[u] = *reinterpret_cast<const uint4*>(src + at);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int at = (u * kCopyThreads + threadIdx.x) * 16;
+    if (at < bytes) *reinterpret_cast<uint4*>(dst + at) = v[u];
+  }
+}
+
+// Page contents of a fork (list of p.n) or a compaction (list of *p.needed, whole pages),
+// over every layer's K and V; after a compaction also the rows of the table.
+template <bool COMPACT>
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagesParams p, const PageLayers layers) {
+  pdl_wait();
+  const int64_t page_bytes = static_cast<int64_t>(p.page_size) * p.token_bytes;
+  const int pieces = static_cast<int>((page_bytes + kCopyBytes - 1) / kCopyBytes);
+  const int n = COMPACT ? *p.needed : p.n;
+  const int64_t work = static_cast<int64_t>(n) * 2 * p.n_layers * pieces;
+  for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+    const int64_t j = w / pieces;
+    const int piece = static_cast<int>(w - j * pieces);
+    const int lk = static_cast<int>(j % (2 * p.n_layers)), m = static_cast<int>(j / (2 * p.n_layers));
+    int src, dst;
+    int64_t bytes;
+    if constexpr (COMPACT) {
+      src = p.movers[n - 1 - m];
+      dst = p.freelist[m];
+      bytes = page_bytes;
+    } else {
+      const int4 c = p.copies[m];
+      src = c.x;
+      dst = c.y;
+      bytes = static_cast<int64_t>(c.z) * p.token_bytes;
+    }
+    const int64_t at = static_cast<int64_t>(piece) * kCopyBytes;
+    if (at >= bytes) continue;
+    char* base = static_cast<char*>(layers.base[lk]);
+    copy_piece(base + src * page_bytes + at, base + dst * page_bytes + at,
+               static_cast<int>(bytes - at < kCopyBytes ? bytes - at : kCopyBytes));
+  }
+  if constexpr (COMPACT) {
+    const int n_live = *p.n_live;
+    const int64_t entries = static_cast<int64_t>(p.n_seqs) * p.pages_per_seq;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
+         e += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+      const int s = static_cast<int>(e / p.pages_per_seq), i = static_cast<int>(e - static_cast<int64_t>(s) * p.pages_per_seq);
+      int pg = p.table[e];
+      if (i < p.held[s]) {
+        if (pg < 0 || pg >= p.n_pages)
+          report(p.status, VG_ERR_DEVICE_BOUNDS);
+        else if (pg >= n_live) {
+          const int to = p.moved_to[pg];
+          if (to >= 0) pg = to;
+          else report(p.status, VG_ERR_DEVICE_BOUNDS);  // a row holds a page that nothing counts
+        }
+      }
+      p.table_out[e] = pg;
+    }
+  }
+}
+
+template <typename K>
+cudaError_t launch_cluster(K* kernel, const PagesParams& p, cudaStream_t stream) {
+  int C = (p.n_pages + kPagesPerCta - 1) / kPagesPerCta;
+  C = C < 1 ? 1 : (C > kPageMaxCluster ? kPageMaxCluster : C);
+  cudaError_t e;
+  if (C > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(kPageThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool COMPACT>
+cudaError_t launch_copy(const PagesParams& p, const PageLayers& layers, int64_t most, int sms, cudaStream_t stream) {
+  const int64_t cap = 8 * static_cast<int64_t>(sms);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < 1 ? 1 : (most < cap ? most : cap)));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_copy_kernel<COMPACT>, p, layers);
+}
+
+int64_t page_pieces(const PagesParams& p) {
+  return (static_cast<int64_t>(p.page_size) * p.token_bytes + kCopyBytes - 1) / kCopyBytes * 2 * p.n_layers;
+}
+
+}  // namespace
+
+cudaError_t launch_pages_request(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream) {
+  const cudaError_t e = launch_cluster(pages_request_kernel, p, stream);
+  if (e != cudaSuccess || !p.copies) return e;
+  return launch_copy<false>(p, layers, p.n * page_pieces(p), sms, stream);
+}
+
+cudaError_t launch_pages_compact(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream) {
+  const cudaError_t e = launch_cluster(pages_compact_kernel, p, stream);
+  if (e != cudaSuccess) return e;
+  return launch_copy<true>(p, layers, static_cast<int64_t>(p.n_pages / 2) * page_pieces(p), sms, stream);
+}
+
+}  // namespace vg

@@ -873,3 +873,326 @@ vg_status vg_sparse_draft_attn_noalloc(const vg_dims* dims, const vg_kv_cache* c
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- rotary positions
+namespace vg {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+vg_status check_rope(const vg_rope* r, int D) {
+  if (!r || !r->freq) return fail(VG_ERR_INVALID_ARG, "rope and its freq must be non-NULL");
+  if (!aligned16(r->freq)) return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (r->rot_dim < 2 || r->rot_dim > D || r->rot_dim % 2 != 0)
+    return fail(VG_ERR_INVALID_ARG, "rot_dim=%d is not an even number in [2, d=%d]", r->rot_dim, D);
+  if (r->layout != VG_ROPE_HALF && r->layout != VG_ROPE_INTERLEAVED)
+    return fail(VG_ERR_INVALID_ARG, "rope layout %d unknown", r->layout);
+  if (!std::isfinite(r->mscale)) return fail(VG_ERR_INVALID_ARG, "mscale must be finite");
+  return VG_OK;
+}
+
+vg_status check_row_stride(int64_t stride, int heads, int D, const char* name) {
+  if (stride % 8 != 0 || stride < static_cast<int64_t>(heads) * D || stride > (int64_t{1} << 40))
+    return fail(VG_ERR_INVALID_ARG, "%s=%lld is not a multiple of 8 of at least %d * %d elements", name,
+                static_cast<long long>(stride), heads, D);
+  return VG_OK;
+}
+
+}  // namespace
+}  // namespace vg
+
+extern "C" {
+
+vg_status vg_rope_freqs(int32_t rot_dim, double base, uint32_t scaling, double factor, double orig_len, double slow,
+                        double fast, uint64_t* freq) {
+  g_err.clear();
+  if (!freq) return fail(VG_ERR_INVALID_ARG, "freq is NULL");
+  if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0)
+    return fail(VG_ERR_INVALID_ARG, "rot_dim=%d is not an even number in [2, 1024]", rot_dim);
+  if (scaling > VG_ROPE_RAMP) return fail(VG_ERR_INVALID_ARG, "rope scaling %u unknown", scaling);
+  if (!(base > 0) || !std::isfinite(base)) return fail(VG_ERR_INVALID_ARG, "base must be positive and finite");
+  if (scaling != VG_ROPE_PLAIN && (!(factor > 0) || !std::isfinite(factor)))
+    return fail(VG_ERR_INVALID_ARG, "factor must be positive and finite");
+  if (scaling == VG_ROPE_RAMP &&
+      (!(orig_len > 0) || !std::isfinite(orig_len) || !(slow >= 0) || !(fast > slow) || !std::isfinite(fast)))
+    return fail(VG_ERR_INVALID_ARG, "ramp scaling needs orig_len > 0 and 0 <= slow < fast");
+  if (scaling == VG_ROPE_BASE && rot_dim > 2) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  const double kTwoPi = 6.283185307179586476925;
+  for (int pass = 0; pass < 2; ++pass) {  // checked first, so that an error leaves freq alone
+    for (int i = 0; i < rot_dim / 2; ++i) {
+      double f = std::pow(base, -2.0 * i / rot_dim);
+      if (scaling == VG_ROPE_LINEAR) f /= factor;
+      if (scaling == VG_ROPE_RAMP) {
+        double w = (orig_len * f / kTwoPi - slow) / (fast - slow);
+        w = w < 0 ? 0 : (w > 1 ? 1 : w);
+        f *= w + (1 - w) / factor;
+      }
+      const double turns = f / kTwoPi;
+      if (!(turns < 1)) return fail(VG_ERR_INVALID_ARG, "frequency %d is %g, a whole turn per position or more", i, f);
+      if (pass == 1) {
+        const double x = std::ldexp(turns, 64);  // below 2^64: turns <= 1 - 2^-53
+        freq[i] = static_cast<uint64_t>(x < 9007199254740992.0 ? std::floor(x + 0.5) : x);
+      }
+    }
+  }
+  return VG_OK;
+}
+
+vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg_rope* rope, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* row_start, int32_t n_rows, const int32_t* prefix_len, void* q_out,
+                         int64_t q_out_stride, int32_t* dev_status, void* stream) {
+  g_err.clear();
+  Shape s;
+  vg_status st = check_dims(dims, &s);
+  if (st != VG_OK) return st;
+  if ((st = check_cache(cache)) != VG_OK) return st;
+  if ((st = check_rope(rope, s.D)) != VG_OK) return st;
+  if (n_rows < 0 || n_rows > (1 << 24)) return fail(VG_ERR_INVALID_ARG, "n_rows=%d outside [0, 2^24]", n_rows);
+  if (!row_start && n_rows != s.B * s.R)
+    return fail(VG_ERR_INVALID_ARG, "n_rows=%d is not B * (gamma + 1) = %d (no row_start)", n_rows, s.B * s.R);
+  if (!q || !k || !v || !q_out || !prefix_len)
+    return fail(VG_ERR_INVALID_ARG, "q, k, v, q_out and prefix_len must be non-NULL");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(prefix_len) ||
+      !aligned16(row_start))
+    return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if ((st = check_row_stride(q_stride, s.Hq, s.D, "q_stride")) != VG_OK) return st;
+  if ((st = check_row_stride(k_stride, s.Hkv, s.D, "k_stride")) != VG_OK) return st;
+  if ((st = check_row_stride(v_stride, s.Hkv, s.D, "v_stride")) != VG_OK) return st;
+  if ((st = check_row_stride(q_out_stride, s.Hq, s.D, "q_out_stride")) != VG_OK) return st;
+  if (q_out == q && q_out_stride != q_stride)
+    return fail(VG_ERR_INVALID_ARG, "q rotated in place needs q_out_stride == q_stride");
+  if (!aligned4(dev_status)) return fail(VG_ERR_INVALID_ARG, "dev_status must be 4-byte aligned");
+  if (n_rows == 0) return VG_OK;
+  DevInfo di;
+  if ((st = device_info(&di)) != VG_OK) return st;
+  RopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.K = static_cast<__nv_bfloat16*>(cache->K);
+  p.V = static_cast<__nv_bfloat16*>(cache->V);
+  p.seq_offset = cache->seq_offset;
+  p.ptab = cache->page_table;
+  p.psize = cache->page_table ? cache->page_size : 1;
+  p.pstride = cache->page_table ? cache->pages_per_seq : 0;
+  p.capacity = cache->capacity_slots;
+  p.row_start = row_start;
+  p.prefix_len = prefix_len;
+  p.freq = rope->freq;
+  p.mscale = rope->mscale != 0.f ? rope->mscale : 1.f;
+  p.rot = rope->rot_dim;
+  p.interleaved = rope->layout == VG_ROPE_INTERLEAVED;
+  p.n_rows = n_rows;
+  p.B = s.B;
+  p.R = s.R;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.D = s.D;
+  p.max_len = s.max_len;
+  p.status = dev_status;
+  const cudaError_t e = launch_rope(p, di.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return VG_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- page pool
+namespace vg {
+namespace {
+
+vg_status check_pool(const vg_page_pool* p) {
+  if (!p || !p->page_table || !p->held || !p->refs)
+    return fail(VG_ERR_INVALID_ARG, "pool and its page_table, held and refs must be non-NULL");
+  if (!aligned16(p->page_table) || !aligned16(p->held) || !aligned16(p->refs))
+    return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (p->n_seqs < 1 || p->n_seqs > 65536) return fail(VG_ERR_INVALID_ARG, "n_seqs=%d outside [1, 65536]", p->n_seqs);
+  if (p->page_size < 1 || p->page_size > (1 << 20))
+    return fail(VG_ERR_INVALID_ARG, "page_size=%d outside [1, 2^20]", p->page_size);
+  if (p->n_pages < 1 || static_cast<int64_t>(p->n_pages) * p->page_size > 0x7fffffffLL)
+    return fail(VG_ERR_INVALID_ARG, "n_pages=%d of %d tokens outside [1, 2^31) slots", p->n_pages, p->page_size);
+  if (p->pages_per_seq < 1 || static_cast<int64_t>(p->n_seqs) * p->pages_per_seq > 0x7fffffffLL)
+    return fail(VG_ERR_INVALID_ARG, "pages_per_seq=%d outside [1, 2^31 / n_seqs)", p->pages_per_seq);
+  return VG_OK;
+}
+
+struct PagesWs {
+  size_t owner, need, have, start, copies, freelist, movers, moved_to, needed, total;
+};
+
+PagesWs pages_ws(const vg_page_pool* p) {
+  PagesWs w = {};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  const size_t rows = static_cast<size_t>(p->n_seqs), pages = static_cast<size_t>(p->n_pages);
+  w.owner = take(rows * 4);
+  w.need = take(rows * 4);
+  w.have = take(rows * 4);
+  w.start = take(rows * 4);
+  w.copies = take(rows * 16);
+  w.freelist = take(pages * 4);
+  w.movers = take(pages * 4);
+  w.moved_to = take(pages * 4);
+  w.needed = take(4);
+  w.total = off;
+  return w;
+}
+
+vg_status check_pages_call(const vg_page_pool* pool, void* ws, size_t ws_bytes, const int32_t* dev_status,
+                           PagesParams* p) {
+  const PagesWs w = pages_ws(pool);
+  if (!ws) return fail(VG_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", w.total);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(VG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < w.total) return fail(VG_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, w.total);
+  if (!aligned4(dev_status)) return fail(VG_ERR_INVALID_ARG, "dev_status must be 4-byte aligned");
+  *p = {};
+  p->table = pool->page_table;
+  p->held = pool->held;
+  p->refs = pool->refs;
+  p->n_seqs = pool->n_seqs;
+  p->pages_per_seq = pool->pages_per_seq;
+  p->n_pages = pool->n_pages;
+  p->page_size = pool->page_size;
+  p->owner = at<int32_t>(ws, w.owner);
+  p->need = at<int32_t>(ws, w.need);
+  p->have = at<int32_t>(ws, w.have);
+  p->start = at<int32_t>(ws, w.start);
+  p->copies = at<int4>(ws, w.copies);
+  p->freelist = at<int32_t>(ws, w.freelist);
+  p->movers = at<int32_t>(ws, w.movers);
+  p->moved_to = at<int32_t>(ws, w.moved_to);
+  p->needed = at<int32_t>(ws, w.needed);
+  return VG_OK;
+}
+
+vg_status check_layers(const vg_page_pool* pool, const vg_kv_cache* caches, int n_layers, int token_bytes,
+                       PagesParams* p, PageLayers* layers) {
+  if (n_layers < 1 || n_layers > kMaxPageLayers)
+    return fail(VG_ERR_UNSUPPORTED_SHAPE, "n_layers=%d outside [1, %d]", n_layers, kMaxPageLayers);
+  if (!caches) return fail(VG_ERR_INVALID_ARG, "caches is NULL");
+  if (token_bytes < 16 || token_bytes > (1 << 20) || token_bytes % 16 != 0)
+    return fail(VG_ERR_INVALID_ARG, "token_bytes=%d is not a multiple of 16 in [16, 2^20]", token_bytes);
+  for (int l = 0; l < n_layers; ++l) {
+    if (!caches[l].K || !caches[l].V) return fail(VG_ERR_INVALID_ARG, "layer %d: K and V must be non-NULL", l);
+    if (!aligned16(caches[l].K) || !aligned16(caches[l].V))
+      return fail(VG_ERR_INVALID_ARG, "layer %d: cache pointers must be 16-byte aligned", l);
+    if (caches[l].capacity_slots < static_cast<int64_t>(pool->n_pages) * pool->page_size)
+      return fail(VG_ERR_INVALID_ARG, "layer %d: capacity_slots=%lld below n_pages * page_size", l,
+                  static_cast<long long>(caches[l].capacity_slots));
+    layers->base[2 * l] = caches[l].K;
+    layers->base[2 * l + 1] = caches[l].V;
+  }
+  p->n_layers = n_layers;
+  p->token_bytes = token_bytes;
+  return VG_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace vg
+
+extern "C" {
+
+size_t vg_pages_workspace_size(const vg_page_pool* pool) {
+  g_err.clear();
+  if (check_pool(pool) != VG_OK) return 0;
+  return pages_ws(pool).total;
+}
+
+vg_status vg_pages_resize(const vg_page_pool* pool, const int32_t* seq, const int32_t* length, int32_t n, void* ws,
+                          size_t ws_bytes, int32_t* dev_status, void* stream) {
+  g_err.clear();
+  vg_status st = check_pool(pool);
+  if (st != VG_OK) return st;
+  if (n < 0 || n > pool->n_seqs) return fail(VG_ERR_INVALID_ARG, "n=%d outside [0, n_seqs=%d]", n, pool->n_seqs);
+  if (!length) return fail(VG_ERR_INVALID_ARG, "length must be non-NULL");
+  if (!aligned16(seq) || !aligned16(length)) return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  PagesParams p;
+  if ((st = check_pages_call(pool, ws, ws_bytes, dev_status, &p)) != VG_OK) return st;
+  if (n == 0) return VG_OK;
+  DevInfo di;
+  if ((st = device_info(&di)) != VG_OK) return st;
+  p.seq = seq;
+  p.length = length;
+  p.n = n;
+  p.copies = nullptr;
+  p.status = dev_status;
+  PageLayers none;
+  const cudaError_t e = launch_pages_request(p, none, di.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "pages launch");
+  return VG_OK;
+}
+
+vg_status vg_pages_fork(const vg_page_pool* pool, const vg_kv_cache* caches, int32_t n_layers, int32_t token_bytes,
+                        const int32_t* parent, const int32_t* child, const int32_t* length, int32_t n, int32_t room,
+                        void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  g_err.clear();
+  vg_status st = check_pool(pool);
+  if (st != VG_OK) return st;
+  if (n < 0 || n > pool->n_seqs) return fail(VG_ERR_INVALID_ARG, "n=%d outside [0, n_seqs=%d]", n, pool->n_seqs);
+  if (room < 0) return fail(VG_ERR_INVALID_ARG, "room=%d < 0", room);
+  if (!parent || !child || !length) return fail(VG_ERR_INVALID_ARG, "parent, child and length must be non-NULL");
+  if (!aligned16(parent) || !aligned16(child) || !aligned16(length))
+    return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  PagesParams p;
+  if ((st = check_pages_call(pool, ws, ws_bytes, dev_status, &p)) != VG_OK) return st;
+  PageLayers layers;
+  if ((st = check_layers(pool, caches, n_layers, token_bytes, &p, &layers)) != VG_OK) return st;
+  if (n == 0) return VG_OK;
+  DevInfo di;
+  if ((st = device_info(&di)) != VG_OK) return st;
+  p.seq = child;
+  p.parent = parent;
+  p.length = length;
+  p.n = n;
+  p.room = room;
+  p.status = dev_status;
+  const cudaError_t e = launch_pages_request(p, layers, di.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "pages launch");
+  return VG_OK;
+}
+
+vg_status vg_pages_compact(const vg_page_pool* pool, const vg_kv_cache* caches, int32_t n_layers, int32_t token_bytes,
+                           int32_t* page_table_out, int32_t* refs_out, int32_t* n_live, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+  g_err.clear();
+  vg_status st = check_pool(pool);
+  if (st != VG_OK) return st;
+  if (!page_table_out || !refs_out || !n_live)
+    return fail(VG_ERR_INVALID_ARG, "page_table_out, refs_out and n_live must be non-NULL");
+  if (!aligned16(page_table_out) || !aligned16(refs_out) || !aligned16(n_live))
+    return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  const size_t tb = static_cast<size_t>(pool->n_seqs) * pool->pages_per_seq * 4, rb = static_cast<size_t>(pool->n_pages) * 4;
+  if ((page_table_out != pool->page_table && overlap(page_table_out, tb, pool->page_table, tb)) ||
+      (refs_out != pool->refs && overlap(refs_out, rb, pool->refs, rb)))
+    return fail(VG_ERR_INVALID_ARG, "page_table_out and refs_out: the pool's own arrays, or no overlap with them");
+  PagesParams p;
+  if ((st = check_pages_call(pool, ws, ws_bytes, dev_status, &p)) != VG_OK) return st;
+  PageLayers layers;
+  if ((st = check_layers(pool, caches, n_layers, token_bytes, &p, &layers)) != VG_OK) return st;
+  DevInfo di;
+  if ((st = device_info(&di)) != VG_OK) return st;
+  p.table_out = page_table_out;
+  p.refs_out = refs_out;
+  p.n_live = n_live;
+  p.status = dev_status;
+  const cudaError_t e = launch_pages_compact(p, layers, di.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "pages launch");
+  return VG_OK;
+}
+
+}  // extern "C"

@@ -114,6 +114,64 @@ struct AcceptParams {
   int32_t* status;
 };
 
+// Rows a rope_kernel CTA takes at a time (each is looked up by a warp of its own).
+constexpr int kRopeMaxRows = 4;
+
+struct RopeParams {
+  const __nv_bfloat16 *q, *k, *v;  // [n_rows][heads][D], row strides in elements
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* K;            // cache [capacity][Hkv][D]
+  __nv_bfloat16* V;
+  const int64_t* seq_offset;   // [B] (slot pool) or null (paged)
+  const int32_t* ptab;         // [B][pstride] page table, or null (slot pool)
+  int psize, pstride;
+  int64_t capacity;
+  const int32_t* row_start;    // [B + 1] or null (R rows a sequence)
+  const int32_t* prefix_len;   // [B]
+  const uint64_t* freq;        // [rot / 2] turns per position, 0.64 fixed point
+  float mscale;                // on every cosine and sine
+  int rot, interleaved;
+  int n_rows, B, R, Hq, Hkv, D, max_len;
+  int32_t* status;
+};
+
+// Layers whose K and V one page call copies.
+constexpr int kMaxPageLayers = 128;
+
+struct PageLayers {
+  void* base[2 * kMaxPageLayers];  // K and V of each layer
+};
+
+struct PagesParams {
+  int32_t* table;  // [n_seqs][pages_per_seq]
+  int32_t* held;   // [n_seqs] pages a row holds
+  int32_t* refs;   // [n_pages] rows that hold a page, 0: free
+  int n_seqs, pages_per_seq, n_pages, page_size;
+  // a request (resize, fork)
+  const int32_t* seq;     // [n] rows named (fork: the children), or null: 0 .. n - 1
+  const int32_t* parent;  // [n], or null (resize)
+  const int32_t* length;  // [n] tokens
+  int n, room;
+  // a compaction
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* n_live;
+  // page contents
+  int token_bytes, n_layers;
+  // workspace
+  int32_t* owner;     // [n_seqs] first request that names a row
+  int32_t* need;      // [n_seqs] pages a request is handed
+  int32_t* have;      // [n_seqs] pages a row keeps or shares, -1: refused
+  int32_t* start;     // [n_seqs] rank of its first page among those handed out
+  int4* copies;       // [n_seqs] (source, destination, tokens, 0), or null
+  int32_t* freelist;  // [n_pages] free pages, ascending
+  int32_t* movers;    // [n_pages] live pages to move, descending
+  int32_t* moved_to;  // [n_pages] where a moved page went (-1: a free one)
+  int32_t* needed;    // pages handed out in all / pages moved
+  int32_t* status;
+};
+
 // Launchers (return a cudaError_t from the launch).
 cudaError_t launch_verify(const VerifyParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           cudaStream_t stream);
@@ -137,5 +195,9 @@ int accept_tiles(int V);   // tiles of the sampling draw over a row of V entries
 // Warps of the draft step's combine kernel (4, 8 or 16 from the most partials a
 // sequence has), or 0 when every sequence's entries sit in one CTA (no combine runs).
 int draft_combine_warps(int B, int slots, int nctas);
+cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream);
+// Grow, cut or fork rows (p.copies: then the copies of a fork's partial pages too).
+cudaError_t launch_pages_request(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream);
 
 }  // namespace vg

@@ -2,8 +2,9 @@
 
 ``LayerState`` owns the torch tensors the C ABI works on: the token-granular KV
 slot pool, per-sequence offsets and lengths, the iteration's inputs, output
-buffers, the workspace and the device status word.  Its methods only marshal
-arguments to libvg.so (via ``binding``); PyTorch serves as the allocator and the
+buffers, the workspace and the device status word.  ``PagePool`` owns the block table,
+page counts and references that the layers of a paged cache share.  Their methods only
+marshal arguments to libvg.so (via ``binding``); PyTorch serves as the allocator and the
 stream provider.
 """
 from __future__ import annotations
@@ -117,6 +118,14 @@ class LayerState:
                                 dev_status=self.status, stream=stream,
                                 flags=vb.VG_DRAFT_SELECTION_SETTLED if settled else 0)
 
+    def rope_append(self, rope: vb.vg_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    q_out: torch.Tensor | None = None, stream=None) -> None:
+        """Rotate the verify rows' q ([B * (gamma + 1)][H_q][d], in place without q_out) and k, and
+        append k and v behind the prefixes (then ``verify(append=False)``)."""
+        q_out = q if q_out is None else q_out
+        vb.vg_rope_append(self.dims, self.cache, rope, q, q.stride(0), k, k.stride(0), v, v.stride(0), None,
+                          q.shape[0], self.prefix_len, q_out, q_out.stride(0), dev_status=self.status, stream=stream)
+
     def launches_per_iteration(self, select_extra: bool = False, tail_from_device: bool = False) -> int:
         """Kernels one iteration enqueues: the verify kernel and its combine, one selection
         (two with select_extra), and each draft step's kernels (vg_iteration gives step s a
@@ -124,6 +133,50 @@ class LayerState:
         draft = sum(vb.vg_sparse_draft_launches(self.dims, self.k, 0 if tail_from_device else s + 1)
                     for s in range(self.gamma))
         return 2 + (2 if select_extra and self.mask1 else 1) + draft
+
+    def check_status(self) -> int:
+        return int(self.status.item())
+
+
+class PagePool:
+    """The pages of a paged cache and the rows that hold them (vg_pages_*), on the device.
+
+    layers: (K, V) tensors [n_pages * page_size][H_kv][d] of each layer; one table serves all."""
+
+    def __init__(self, n_seqs: int, pages_per_seq: int, n_pages: int, page_size: int, layers):
+        self.layers = list(layers)
+        K = self.layers[0][0]
+        dev = K.device
+        self.page_size = page_size
+        self.token_bytes = K[0].numel() * K.element_size()
+        self.page_table = torch.full((n_seqs, pages_per_seq), -1, dtype=torch.int32, device=dev)
+        self.held = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.refs = torch.zeros(n_pages, dtype=torch.int32, device=dev)
+        self.n_live = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.pool = vb.make_pages(self.page_table, self.held, self.refs, page_size)
+        self.caches = vb.make_caches(self.layers)
+        self.ws = torch.empty(vb.vg_pages_workspace_size(self.pool), dtype=torch.uint8, device=dev)
+
+    def cache(self, layer: int = 0) -> vb.vg_kv_cache:
+        """Layer `layer` as a paged cache whose sequences are the table's first rows."""
+        K, V = self.layers[layer]
+        return vb.make_cache(K, V, None, page_table=self.page_table, page_size=self.page_size)
+
+    def resize(self, seq: torch.Tensor | None, length: torch.Tensor, stream=None) -> None:
+        """Rows seq (None: the first ones) hold length tokens each; 0 frees a row."""
+        vb.vg_pages_resize(self.pool, seq, length, length.numel(), self.ws, dev_status=self.status, stream=stream)
+
+    def fork(self, parent: torch.Tensor, child: torch.Tensor, length: torch.Tensor, room: int = 0,
+             stream=None) -> None:
+        """Rows child become branches of the first length tokens of rows parent."""
+        vb.vg_pages_fork(self.pool, self.caches, self.token_bytes, parent, child, length, length.numel(), room,
+                         self.ws, dev_status=self.status, stream=stream)
+
+    def compact(self, stream=None) -> None:
+        """Move the live pages to the front of the pool, in place (n_live: how many)."""
+        vb.vg_pages_compact(self.pool, self.caches, self.token_bytes, self.page_table, self.refs, self.n_live,
+                            self.ws, dev_status=self.status, stream=stream)
 
     def check_status(self) -> int:
         return int(self.status.item())
