@@ -19,6 +19,7 @@
  *   vg_iteration_plan_*   the same iteration captured once as a CUDA graph and
  *                         launched step after step.
  * Around a batch of such sequences:
+ *   vg_shared_verify_attn verification for sequences that share a prefix, read once for all;
  *   vg_rope_append        rotary positions of new q and k rows; k and v enter the cache;
  *   vg_pages_resize, vg_pages_fork, vg_pages_compact
  *                         the page pool behind a block table: rows grown, cut and freed,
@@ -337,6 +338,42 @@ vg_status vg_accept(int32_t B, int32_t gamma, int32_t V, const float* p_logits, 
                     const int32_t* draft_tokens, const float* u_accept, const float* u_resample,
                     uint32_t mode, int32_t* n_accept, int32_t* next_token, int32_t* advance_len,
                     void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * vg_verify_attn for a batch whose sequences share prefixes: samples, branches or requests of
+ * one prompt.  No counterpart in the page, which treats each sequence by itself; the results
+ * are those of vg_verify_attn (up to rounding), the shared tokens' keys and values being read
+ * once for a whole group instead of once a sequence.
+ *
+ *   groups->n_groups     groups of consecutive sequences, 1 .. 1024
+ *   groups->group_start  device int32 [n_groups + 1], ascending from 0 to B: group j is
+ *                        sequences group_start[j] .. group_start[j + 1] - 1 (it may be empty);
+ *                        NULL with n_groups == 1: the whole batch
+ *   groups->shared_len   device int32 [n_groups]: the first shared_len[j] tokens of all members
+ *                        are the same, 0 <= shared_len[j] <= every member's prefix_len.  They
+ *                        are read where the group's first member has them; a remainder past a
+ *                        multiple of 128 tokens is read where each member has it, so every
+ *                        member's own table row (or slots) must hold all of its tokens, as
+ *                        after vg_pages_fork.
+ *   row_mask, scores     as row_mask0, scores0 of vg_verify_attn: scores for every prefix entry
+ *                        of every sequence, shared ones included; both 0 / NULL to leave out
+ *   others               as vg_verify_attn (page_size 8, 16, 32 or a multiple of 64)
+ * A group_start that is not such a list, or a shared_len out of range, is reported as
+ * VG_ERR_DEVICE_BOUNDS, and the group's (or every) sequence is then read by itself.
+ * Workspace: at least vg_shared_verify_workspace_size(dims, groups) bytes (only n_groups is
+ * read; 0 on bad arguments or no device), 256-byte aligned, contents arbitrary.
+ * Launches: 2, or 4 with scores.
+ */
+typedef struct vg_prefix_groups {
+  int32_t n_groups;
+  const int32_t* group_start;
+  const int32_t* shared_len;
+} vg_prefix_groups;
+size_t vg_shared_verify_workspace_size(const vg_dims* dims, const vg_prefix_groups* groups);
+vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, const vg_prefix_groups* groups,
+                                const void* q, const void* k_new, const void* v_new, const int32_t* prefix_len,
+                                uint32_t row_mask, float* scores, int64_t score_stride, void* out, void* ws,
+                                size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /*
  * Rotary positions of new q and k rows, and the append of k and v to the cache.  No

@@ -27,7 +27,7 @@ ENTRY_POINTS = ("vg_verify_attn", "vg_topk_select", "vg_window_select", "vg_spar
                 "vg_iteration_plan_create", "vg_iteration_plan_launch", "vg_iteration_plan_destroy",
                 "vg_sparse_draft_attn_noalloc", "vg_workspace_size", "vg_sparse_draft_launches",
                 "vg_accept", "vg_accept_workspace_size",
-                "vg_rope_append", "vg_rope_freqs", "vg_pages_resize", "vg_pages_fork", "vg_pages_compact",
+                "vg_shared_verify_attn", "vg_shared_verify_workspace_size", "vg_rope_append", "vg_rope_freqs", "vg_pages_resize", "vg_pages_fork", "vg_pages_compact",
                 "vg_pages_workspace_size",
                 "vg_last_error", "vg_version", "vg_selftest_lost_wait")
 
@@ -60,6 +60,10 @@ class vg_iter_outputs(ctypes.Structure):
     _fields_ = [("out_verify", ctypes.c_void_p), ("scores0", ctypes.c_void_p), ("scores1", ctypes.c_void_p),
                 ("score_stride", ctypes.c_int64), ("idx", ctypes.c_void_p), ("count", ctypes.c_void_p),
                 ("idx1", ctypes.c_void_p), ("count1", ctypes.c_void_p), ("out_draft", ctypes.c_void_p)]
+
+
+class vg_prefix_groups(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("group_start", ctypes.c_void_p), ("shared_len", ctypes.c_void_p)]
 
 
 class vg_rope(ctypes.Structure):
@@ -119,6 +123,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.vg_sparse_draft_launches.argtypes = [ctypes.POINTER(vg_dims), i32, i32]
     L.vg_sparse_draft_launches.restype = i32
     f64 = ctypes.c_double
+    L.vg_shared_verify_workspace_size.argtypes = [ctypes.POINTER(vg_dims), ctypes.POINTER(vg_prefix_groups)]
+    L.vg_shared_verify_workspace_size.restype = sz
+    L.vg_shared_verify_attn.argtypes = [ctypes.POINTER(vg_dims), ctypes.POINTER(vg_kv_cache),
+                                        ctypes.POINTER(vg_prefix_groups), vp, vp, vp, vp, u32, vp, i64, vp, vp, sz, vp,
+                                        vp]
+    L.vg_shared_verify_attn.restype = i32
     L.vg_rope_append.argtypes = [ctypes.POINTER(vg_dims), ctypes.POINTER(vg_kv_cache), ctypes.POINTER(vg_rope), vp, i64,
                                  vp, i64, vp, i64, vp, i32, vp, vp, i64, vp, vp]
     L.vg_rope_append.restype = i32
@@ -278,6 +288,28 @@ def vg_sparse_draft_attn_noalloc(dims, cache, q, k_new, v_new, idx, count, k_str
     _check(load().vg_sparse_draft_attn_noalloc(ctypes.byref(dims), ctypes.byref(cache), ptr(q), ptr(k_new),
                                                ptr(v_new), ptr(idx), ptr(count), k_stride, ptr(tail_start),
                                                ptr(tail_len), ptr(out), ptr(dev_status), _stream(stream)))
+
+
+def make_groups(group_start, shared_len) -> vg_prefix_groups:
+    """Groups of consecutive sequences and the tokens each shares: int32 tensors group_start
+    [n_groups + 1] (None: one group of the whole batch) and shared_len [n_groups]."""
+    return vg_prefix_groups(shared_len.shape[0], ptr(group_start), ptr(shared_len))
+
+
+def vg_shared_verify_workspace_size(dims: vg_dims, groups: vg_prefix_groups) -> int:
+    n = load().vg_shared_verify_workspace_size(ctypes.byref(dims), ctypes.byref(groups))
+    if n == 0:
+        raise VgError(VG_ERR_INVALID_ARG, load().vg_last_error().decode())
+    return n
+
+
+def vg_shared_verify_attn(dims, cache, groups: vg_prefix_groups, q, k_new, v_new, prefix_len, row_mask, scores,
+                          score_stride, out, ws, ws_bytes=None, dev_status=None, stream=None) -> None:
+    """vg_verify_attn for groups of sequences that share a prefix, read once for each group."""
+    wsb = ws_bytes if ws_bytes is not None else (ws.numel() * ws.element_size() if ws is not None else 0)
+    _check(load().vg_shared_verify_attn(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(groups), ptr(q),
+                                        ptr(k_new), ptr(v_new), ptr(prefix_len), row_mask, ptr(scores), score_stride,
+                                        ptr(out), ptr(ws), wsb, ptr(dev_status), _stream(stream)))
 
 
 VG_ROPE_HALF = 0

@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libvg.so")
 
 SOURCES = ["vg_api.cu", "verify_attn.cu", "topk_select.cu", "sparse_draft.cu", "accept.cu",
-           "rope.cu", "pages.cu"]
+           "shared_attn.cu", "rope.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

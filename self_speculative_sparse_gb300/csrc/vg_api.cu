@@ -1196,3 +1196,142 @@ vg_status vg_pages_compact(const vg_page_pool* pool, const vg_kv_cache* caches, 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- shared prefixes
+namespace vg {
+namespace {
+
+struct SharedWs {
+  size_t meta, parts_o, parts_ml, partp_o, partp_ml, qsum, total;
+  int64_t items;  // shared and private items at most
+};
+
+SharedWs shared_ws(const Shape& s, int n_groups, int sms) {
+  SharedWs w = {};
+  const int64_t rows = static_cast<int64_t>(s.B) * s.M, ng = n_groups, Hp = (s.Hkv + 1) / 2;
+  // pairs of row tiles over all groups: floor(ceil(rows_g / 128) / 2) each, which is at most
+  // (rows_g + 127) / 256, and nothing below 129 rows
+  const int64_t by_tile = (rows + 127 * ng) / 256, by_rows = rows / 129;
+  const int64_t pairs = by_tile < by_rows ? by_tile : by_rows;
+  const int64_t shared = s.Hkv * pairs + Hp * (ng < s.B ? ng : s.B);
+  const int64_t priv = s.B * Hp;
+  w.items = shared + priv;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  const size_t srows = static_cast<size_t>(sms + shared) * 2 * kSharedTileKeys;
+  const size_t prows = static_cast<size_t>(sms + priv) * 2 * s.Mpad;
+  w.meta = take(static_cast<size_t>(shared_meta_ints(s.B, n_groups)) * 4);
+  w.parts_o = take(srows * s.D * 4);
+  w.parts_ml = take(srows * 8);
+  w.partp_o = take(prows * s.D * 4);
+  w.partp_ml = take(prows * 8);
+  w.qsum = take(static_cast<size_t>(3) * ((s.B + 15) & ~15) * s.Hkv * s.D * 2);
+  w.total = off;
+  return w;
+}
+
+vg_status check_groups(const vg_prefix_groups* g) {
+  if (!g) return fail(VG_ERR_INVALID_ARG, "groups is NULL");
+  if (g->n_groups < 1 || g->n_groups > kMaxBatch)
+    return fail(VG_ERR_INVALID_ARG, "n_groups=%d outside [1, %d]", g->n_groups, kMaxBatch);
+  return VG_OK;
+}
+
+}  // namespace
+}  // namespace vg
+
+extern "C" {
+
+size_t vg_shared_verify_workspace_size(const vg_dims* dims, const vg_prefix_groups* groups) {
+  g_err.clear();
+  Shape s;
+  if (check_dims(dims, &s) != VG_OK || check_groups(groups) != VG_OK) return 0;
+  DevInfo di;
+  if (device_info(&di) != VG_OK) return 0;
+  return shared_ws(s, groups->n_groups, di.sms).total;
+}
+
+vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, const vg_prefix_groups* groups,
+                                const void* q, const void* k_new, const void* v_new, const int32_t* prefix_len,
+                                uint32_t row_mask, float* scores, int64_t score_stride, void* out, void* ws,
+                                size_t ws_bytes, int32_t* dev_status, void* stream) {
+  g_err.clear();
+  Shape s;
+  vg_status st = check_dims(dims, &s);
+  if (st != VG_OK) return st;
+  if ((st = check_cache(cache)) != VG_OK) return st;
+  if ((st = check_verify_pages(cache)) != VG_OK) return st;
+  if ((st = check_groups(groups)) != VG_OK) return st;
+  if (!groups->shared_len || (groups->n_groups > 1 && !groups->group_start))
+    return fail(VG_ERR_INVALID_ARG, "shared_len (and, with several groups, group_start) must be non-NULL");
+  if (!aligned16(groups->shared_len) || !aligned16(groups->group_start))
+    return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  VerifyArgs a{q, k_new, v_new, prefix_len, row_mask, 0, scores, nullptr, score_stride, out};
+  if ((st = check_verify_args(s, a)) != VG_OK) return st;
+  if (!aligned4(dev_status)) return fail(VG_ERR_INVALID_ARG, "dev_status must be 4-byte aligned");
+  DevInfo di;
+  if ((st = device_info(&di)) != VG_OK) return st;
+  const SharedWs w = shared_ws(s, groups->n_groups, di.sms);
+  if (w.items * (s.max_len / kSharedTileKeys + 1) > 0x7fffffffLL)
+    return fail(VG_ERR_UNSUPPORTED_SHAPE, "B=%d sequences of up to max_len=%d tokens are too many tiles", s.B, s.max_len);
+  if (!ws) return fail(VG_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", w.total);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(VG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < w.total) return fail(VG_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, w.total);
+  SharedParams p = {};
+  p.nslots = shared_slots(s.D, s.B, groups->n_groups, di.smem_optin);
+  if (p.nslots < 4) return fail(VG_ERR_UNSUPPORTED_SHAPE, "too little shared memory for B=%d", s.B);
+  p.Bpad = (s.B + 15) & ~15;
+  p.qsum = at<__nv_bfloat16>(ws, w.qsum);
+  CUtensorMap tmK, tmV, tmZ;
+  if ((st = encode_cache_map(&tmK, cache->K, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
+  if ((st = encode_cache_map(&tmV, cache->V, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
+  tmZ = tmK;
+  if (row_mask && (st = encode_cache_map(&tmZ, p.qsum, 3 * p.Bpad, s.Hkv, s.D, 16)) != VG_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.K = static_cast<__nv_bfloat16*>(cache->K);
+  p.V = static_cast<__nv_bfloat16*>(cache->V);
+  p.seq_offset = cache->seq_offset;
+  p.ptab = cache->page_table;
+  p.psize = cache->page_table ? cache->page_size : 1;
+  p.pstride = cache->page_table ? cache->pages_per_seq : 0;
+  p.box_rows = verify_box_rows(cache);
+  p.capacity = cache->capacity_slots;
+  p.prefix_len = prefix_len;
+  p.group_start = groups->group_start;
+  p.shared_len = groups->shared_len;
+  p.n_groups = groups->n_groups;
+  p.B = s.B;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.G = s.G;
+  p.R = s.R;
+  p.D = s.D;
+  p.M = s.M;
+  p.Mpad = s.Mpad;
+  p.max_len = s.max_len;
+  p.scale = s.scale;
+  p.scale_log2 = s.scale * 1.4426950408889634f;
+  p.mask = row_mask;
+  p.nsc = s.B <= 16 ? 16 : 64;
+  p.nctas = di.sms;
+  p.meta = at<int32_t>(ws, w.meta);
+  p.parts_o = at<float>(ws, w.parts_o);
+  p.parts_ml = at<float>(ws, w.parts_ml);
+  p.partp_o = at<float>(ws, w.partp_o);
+  p.partp_ml = at<float>(ws, w.partp_ml);
+  p.scores = scores;
+  p.score_stride = score_stride;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.status = dev_status;
+  const cudaError_t e = launch_shared(p, tmK, tmV, tmZ, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "shared verify launch");
+  return VG_OK;
+}
+
+}  // extern "C"

@@ -114,6 +114,45 @@ struct AcceptParams {
   int32_t* status;
 };
 
+// Keys of a tile of the shared-prefix kernels, and the rows of one lane's tile.
+constexpr int kSharedTileKeys = 128;
+
+struct SharedParams {
+  const __nv_bfloat16* q;      // [B][R][Hq][D]
+  const __nv_bfloat16* k_new;  // [B][R][Hkv][D] or null (read from the cache)
+  const __nv_bfloat16* v_new;
+  __nv_bfloat16* K;            // cache [capacity][Hkv][D]
+  __nv_bfloat16* V;
+  const int64_t* seq_offset;   // [B] (slot pool) or null (paged)
+  const int32_t* ptab;         // [B][pstride] page table, or null (slot pool)
+  int psize, pstride;
+  int box_rows;                // rows of one K/V TMA box: 64 for the slot pool, else min(page size, 64)
+  int64_t capacity;
+  const int32_t* prefix_len;   // [B]
+  const int32_t* group_start;  // [n_groups + 1], or null: one group
+  const int32_t* shared_len;   // [n_groups]
+  int n_groups;
+  int B, Hq, Hkv, G, R, D, M, Mpad;  // M = G * R rows per (sequence, KV head), Mpad = 16 * ceil(M / 16)
+  int max_len;
+  float scale, scale_log2;
+  uint32_t mask;               // verify rows summed into scores (0: no scores)
+  int nsc;                     // members of one score item: 16 or 64
+  int Bpad;                    // rows of one part of qsum: B rounded up to 16
+  int nctas, nslots;           // attention grid; ring slots of a CTA
+  // workspace
+  int32_t* meta;         // the batch's layout (shared_meta_ints)
+  float* parts_o;        // [nctas + shared items][2][128][D] unnormalised partial outputs
+  float* parts_ml;       // [...][2] (running max in log2 units, sum)
+  float* partp_o;        // [nctas + private items][2][Mpad][D]
+  float* partp_ml;
+  __nv_bfloat16* qsum;   // [3][Bpad][Hkv * D] the masked rows' summed queries, in three parts
+  // outputs
+  float* scores;         // [B][score_stride] or null
+  int64_t score_stride;
+  __nv_bfloat16* out;    // [B][R][Hq][D]
+  int32_t* status;
+};
+
 // Rows a rope_kernel CTA takes at a time (each is looked up by a warp of its own).
 constexpr int kRopeMaxRows = 4;
 
@@ -195,6 +234,11 @@ int accept_tiles(int V);   // tiles of the sampling draw over a row of V entries
 // Warps of the draft step's combine kernel (4, 8 or 16 from the most partials a
 // sequence has), or 0 when every sequence's entries sit in one CTA (no combine runs).
 int draft_combine_warps(int B, int slots, int nctas);
+// tmZ: qsum as rows of Hkv * D, boxes of 64 columns x 16 rows (unused without scores)
+cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          const CUtensorMap& tmZ, cudaStream_t stream);
+int shared_meta_ints(int B, int n_groups);
+int shared_slots(int D, int B, int n_groups, size_t smem_optin);  // ring slots that fit a CTA
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream);
 // Grow, cut or fork rows (p.copies: then the copies of a fork's partial pages too).
 cudaError_t launch_pages_request(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream);

@@ -118,6 +118,13 @@ class LayerState:
                                 dev_status=self.status, stream=stream,
                                 flags=vb.VG_DRAFT_SELECTION_SETTLED if settled else 0)
 
+    def verify_shared(self, groups: vb.vg_prefix_groups, ws: torch.Tensor, stream=None, append: bool = True) -> None:
+        """``verify`` for groups that share a prefix (vb.make_groups); ws: scratch of
+        vb.vg_shared_verify_workspace_size(self.dims, groups) bytes.  Fills out_verify and scores0."""
+        vb.vg_shared_verify_attn(self.dims, self.cache, groups, self.q_verify, self.k_new if append else None,
+                                 self.v_new if append else None, self.prefix_len, self.mask0, self.scores0,
+                                 self.score_stride, self.out_verify, ws, dev_status=self.status, stream=stream)
+
     def rope_append(self, rope: vb.vg_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     q_out: torch.Tensor | None = None, stream=None) -> None:
         """Rotate the verify rows' q ([B * (gamma + 1)][H_q][d], in place without q_out) and k, and

@@ -176,3 +176,38 @@ def test_oracle_pool_shares_copies_and_runs_out():
     assert p.rows[3] == [2, 4, 5] and p.refs == [2, 2, 1, 1, 1, 1]
     p.resize([1, 2], [0, 0])
     assert p.compact() == [(4, 0), (5, 1)] and p.rows[3] == [2, 0, 1]
+
+
+# ------------------------------------------------------------ shared prefixes
+def shared_call(lib, d=None, c=None, ng=2, start=A, shared=A, groups=True, q=A, kn=A, vn=A, prefix=A, mask=0x9, scores=A,
+                stride=512, out=A, ws=A, ws_bytes=1 << 40, status=None):
+    d = dims() if d is None else d
+    c = cache() if c is None else c
+    g = vb.vg_prefix_groups(ng, vb.ptr(start), vb.ptr(shared))
+    return lib.vg_shared_verify_attn(ctypes.byref(d), ctypes.byref(c), ctypes.byref(g) if groups else None, vb.ptr(q),
+                                     vb.ptr(kn), vb.ptr(vn), vb.ptr(prefix), mask, vb.ptr(scores), stride, vb.ptr(out),
+                                     vb.ptr(ws), ws_bytes, vb.ptr(status), None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(groups=False), dict(ng=0), dict(ng=1025), dict(start=None), dict(shared=None), dict(start=MIS), dict(shared=MIS),
+    dict(q=None), dict(prefix=None), dict(out=None), dict(kn=None), dict(vn=None), dict(q=MIS), dict(out=MIS),
+    dict(mask=0x10), dict(mask=0), dict(scores=None), dict(stride=511), dict(scores=MIS), dict(status=Buf(0x10002)),
+    dict(d=dims(max_len=-1)),
+])
+def test_shared_refusals(lib, bad):
+    assert shared_call(lib, **bad) == vb.VG_ERR_INVALID_ARG
+    assert lib.vg_last_error()
+
+
+def test_shared_unsupported_shapes_and_no_gpu(lib):
+    import torch
+    assert shared_call(lib, d=dims(d=80)) == vb.VG_ERR_UNSUPPORTED_SHAPE
+    assert shared_call(lib, d=dims(gamma=16)) == vb.VG_ERR_UNSUPPORTED_SHAPE
+    odd = vb.vg_kv_cache(A.addr, A.addr, None, 4096, A.addr, 24, 30)
+    assert shared_call(lib, c=odd) == vb.VG_ERR_UNSUPPORTED_SHAPE
+    if not torch.cuda.is_available():
+        assert shared_call(lib) == vb.VG_ERR_CUDA
+        assert shared_call(lib, ng=1, start=None) == vb.VG_ERR_CUDA
+        g = vb.vg_prefix_groups(1, None, A.addr)
+        assert lib.vg_shared_verify_workspace_size(ctypes.byref(dims()), ctypes.byref(g)) == 0
