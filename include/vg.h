@@ -362,7 +362,7 @@ vg_status vg_accept(int32_t B, int32_t gamma, int32_t V, const float* p_logits, 
  * VG_ERR_DEVICE_BOUNDS, and the group's (or every) sequence is then read by itself.
  * Workspace: at least vg_shared_verify_workspace_size(dims, groups) bytes (only n_groups is
  * read; 0 on bad arguments or no device), 256-byte aligned, contents arbitrary.
- * Launches: 2, or 4 with scores.
+ * Launches: 3, or 4 with scores.
  */
 typedef struct vg_prefix_groups {
   int32_t n_groups;

@@ -13,7 +13,7 @@
 // them), so the tall problem needs no mask at all.
 //
 // Attention kernel.  One persistent CTA per SM; the flattened list of steps is split evenly
-// over the CTAs.  A CTA has two softmax warpgroups, "lanes", each with its own 128 rows, S / P
+// over the CTAs.  A CTA has two "lanes" of eight softmax warps, each with its own 128 rows, S / P
 // and O in tensor memory; a step is one key tile for both lanes:
 //   pair   the lanes are two row tiles of one KV head and share the step's K and V tile;
 //   heads  the lanes are the same row tile of two KV heads, each with its own K and V tile
@@ -21,8 +21,8 @@
 // While one lane's warps run the softmax of their tile, the tensor cores work for the other
 // (P V of its tile, then Q K^T of its next).  P goes back to tensor memory as bf16, over the
 // columns of S, and is the A operand of P V from there: it never passes shared memory.
-// Warps: 0-3 and 4-7 the lanes (a thread is a row: no exchange between threads), 8 the TMA
-// producer, 9 the MMA issuer.
+// Warps: 0-7 and 8-15 the lanes (two threads a row), 16 and 18 the TMA producers, 17 and 19
+// the lanes' MMA issuers.
 #include "vg_common.cuh"
 #include "vg_internal.h"
 
@@ -34,11 +34,16 @@ static_assert(KT == 128, "a lane's rows and a tile's keys are the 128 tensor-mem
 // A row's running max is raised only when a tile exceeds it by more than this (log2 units):
 // P stays below 2^8 and O is rescaled rarely.
 constexpr float kRescaleSlack = 8.f;
-constexpr int kMaxSlots = 12;  // ring slots (K or V tiles)
+constexpr int kMaxSlots = 12;  // ring slots (K or V tiles) at most
 
 // ---------------------------------------------------------------- the batch's layout
-// Everything the kernels need about lengths and groups, from the device arrays; built by one
-// warp of each CTA (B <= 1024), and left in the workspace for the combine kernel.
+// Everything the kernels need about lengths and groups, in the workspace: built from the
+// device arrays by one CTA of a first small kernel, copied to shared memory by the others.
+// An item is one unit of rows (a pair of row tiles of a KV head, or one row tile of two KV
+// heads) and its whole key range.  The attention CTAs split the items' steps evenly, an item
+// counting one step more than its key tiles: filling and draining its pipeline costs a CTA
+// about as much as a tile, and without that step the CTAs at the short private ranges were
+// the last to finish.
 struct Meta {
   int* gs;     // [ng + 1] first sequence of a group
   int* eff;    // [ng + 1] tokens of a group read once (a multiple of 128)
@@ -67,118 +72,40 @@ __device__ __forceinline__ Meta meta_at(int* base, int B, int ng) {
   return m;
 }
 
-__device__ __forceinline__ int warp_incl(int v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  return v;
-}
-
 // Row tiles of a group's KV head: `pairs` pairs of them, and whether one is left over.
-__device__ __forceinline__ void row_tiles(int members, int M, int& pairs, int& odd) {
-  const int rt = (members * M + KT - 1) / KT;
+__device__ __forceinline__ void row_tiles(int members, const SharedParams& p, int& pairs, int& odd) {
+  const int rt = (members * p.M + p.RT - 1) / p.RT;
   pairs = rt >> 1;
   odd = rt & 1;
 }
 
-// One warp.
-__device__ void build_meta(const SharedParams& p, const Meta& m) {
-  const int lane = threadIdx.x & 31;
-  const int B = p.B, ng = p.n_groups, Hp = (p.Hkv + 1) / 2;
-  bool bad = false;
-  for (int b = lane; b < B; b += 32) {
-    int n = p.prefix_len[b];
-    bool ok = n >= 0 && n <= p.max_len;
-    if (ok) {
-      if (p.ptab) {
-        ok = static_cast<int64_t>(n) + p.R <= static_cast<int64_t>(p.pstride) * p.psize;
-      } else {
-        const int64_t off = p.seq_offset[b];
-        ok = off >= 0 && off + static_cast<int64_t>(n) + p.R <= p.capacity;
-      }
+constexpr int kPrepThreads = 1024;  // a thread a sequence, and a group (at most 1024 of each)
+
+// Exclusive scan over the CTA's threads; *total gets the sum.  All threads.
+__device__ int prep_scan(int v, int* sh, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += t;
     }
-    bad |= !ok;
-    m.nlen[b] = ok ? n : -1;
-    m.grp[b] = 0;
+    sh[lane] = y;
   }
-  bool shape_ok = true;
-  for (int g = lane; g <= ng; g += 32) {
-    const int v = p.group_start ? p.group_start[g] : (g ? B : 0);
-    const int next = g < ng ? (p.group_start ? p.group_start[g + 1] : B) : B;
-    shape_ok &= v >= 0 && v <= next && next <= B && (g > 0 || v == 0) && (g < ng || v == B);
-    m.gs[g] = v;
-  }
-  shape_ok = __all_sync(0xffffffffu, shape_ok);
-  __syncwarp();
-  int c0 = 0, c1 = 0, c2 = 0;
-  for (int g0 = 0; g0 < ng; g0 += 32) {
-    const int g = g0 + lane;
-    int steps = 0, items = 0, sc = 0;
-    if (g < ng) {
-      int eff = 0;
-      if (shape_ok) {
-        const int s0 = m.gs[g], s1 = m.gs[g + 1];
-        if (s0 < s1) {
-          const int shared = p.shared_len[g];
-          int least = 0x7fffffff;
-          for (int b = s0; b < s1; ++b) {
-            m.grp[b] = g;
-            if (m.nlen[b] >= 0) least = min(least, m.nlen[b]);
-          }
-          if (m.nlen[s0] < 0) least = 0;  // no row to read the prefix through (reported above)
-          else if (shared < 0 || shared > least) {
-            bad = true;
-            least = 0;
-          }
-          eff = min(shared, least) / KT * KT;
-          int pairs, odd;
-          row_tiles(s1 - s0, p.M, pairs, odd);
-          const int tiles = eff / KT;
-          items = tiles ? p.Hkv * pairs + odd * Hp : 0;
-          steps = tiles * items;
-          sc = tiles * ((s1 - s0 + p.nsc - 1) / p.nsc);
-        }
-      }
-      m.eff[g] = eff;
-    }
-    const int a = warp_incl(steps), b = warp_incl(items), c = warp_incl(sc);
-    if (g < ng) {
-      m.stepS[g] = c0 + a - steps;
-      m.itemS[g] = c1 + b - items;
-      m.scS[g] = c2 + c - sc;
-    }
-    c0 += __shfl_sync(0xffffffffu, a, 31);
-    c1 += __shfl_sync(0xffffffffu, b, 31);
-    c2 += __shfl_sync(0xffffffffu, c, 31);
-  }
-  if (lane == 0) {
-    m.eff[ng] = 0;
-    m.stepS[ng] = c0;
-    m.itemS[ng] = c1;
-    m.scS[ng] = c2;
-  }
-  __syncwarp();
-  c0 = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    int tiles = 0;
-    if (b < B && m.nlen[b] >= 0) tiles = (m.nlen[b] - m.eff[m.grp[b]] + KT - 1) / KT;
-    const int a = warp_incl(tiles);
-    if (b < B) {
-      m.scP[b] = c0 + a - tiles;
-      m.stepP[b] = (c0 + a - tiles) * Hp;
-    }
-    c0 += __shfl_sync(0xffffffffu, a, 31);
-  }
-  if (lane == 0) {
-    m.scP[B] = c0;
-    m.stepP[B] = c0 * Hp;
-  }
-  if (bad || !shape_ok) report(p.status, VG_ERR_DEVICE_BOUNDS);
-  __syncwarp();
+  __syncthreads();
+  const int r = (warp > 0 ? sh[warp - 1] : 0) + x - v;
+  *total = sh[31];
+  __syncthreads();
+  return r;
 }
 
 // Last index i in [0, n) with cum[i] <= x, skipping empty entries (cum[i] == cum[i + 1]).
@@ -189,6 +116,123 @@ __device__ __forceinline__ int find(const int* cum, int n, int x) {
     if (cum[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// One CTA: the layout.  The other CTAs (with scores), one a sequence: the sum of its masked
+// query rows of each KV head, in fp32, as three bf16 parts whose sum is it to 2^-24.
+__global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const SharedParams p) {
+  __shared__ int gs[kMaxBatch + 1], least[kMaxBatch], eff_of[kMaxBatch], nlen[kMaxBatch], sh[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const int b = blockIdx.x - 1, width = p.Hkv * p.D;
+    const size_t part = static_cast<size_t>(p.Bpad) * width;
+    for (int e = tid; e < width; e += kPrepThreads) {
+      const int g = e / p.D, d = e - g * p.D;
+      float acc = 0.f;
+      for (uint32_t bits = p.mask; bits != 0u; bits &= bits - 1u) {
+        const int t = __ffs(bits) - 1;
+        const __nv_bfloat16* src = p.q + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G) * p.D + d;
+#pragma unroll 4
+        for (int h = 0; h < p.G; ++h) acc += __bfloat162float(src[h * p.D]);
+      }
+      __nv_bfloat16* dst = p.qsum + static_cast<size_t>(b) * width + e;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(acc);
+        dst[k * part] = h;
+        acc -= __bfloat162float(h);
+      }
+    }
+    return;
+  }
+  const int B = p.B, ng = p.n_groups, Hp = (p.Hkv + 1) / 2;
+  const Meta m = meta_at(p.meta, B, ng);
+  bool bad = false;
+  int n = -1, shared = 0;
+  if (tid < B) {
+    n = p.prefix_len[tid];
+    bool ok = n >= 0 && n <= p.max_len;
+    if (ok) {
+      if (p.ptab) {
+        ok = static_cast<int64_t>(n) + p.R <= static_cast<int64_t>(p.pstride) * p.psize;
+      } else {
+        const int64_t off = p.seq_offset[tid];
+        ok = off >= 0 && off + static_cast<int64_t>(n) + p.R <= p.capacity;
+      }
+    }
+    bad = !ok;
+    if (!ok) n = -1;
+    nlen[tid] = n;
+  }
+  if (tid < ng) {
+    gs[tid] = p.group_start ? p.group_start[tid] : 0;
+    shared = p.shared_len[tid];
+    least[tid] = 0x7fffffff;
+  }
+  if (tid == 0) gs[ng] = p.group_start ? p.group_start[ng] : B;
+  __syncthreads();
+  bool shape = true;
+  if (tid < ng) shape = gs[tid] >= 0 && gs[tid] <= gs[tid + 1] && gs[tid + 1] <= B;
+  if (tid == 0) shape = shape && gs[0] == 0 && gs[ng] == B;
+  shape = __syncthreads_and(shape);
+  int grp = 0;
+  if (tid < B && shape) {
+    grp = find(gs, ng, tid);
+    if (n >= 0) atomicMin(&least[grp], n);
+  }
+  __syncthreads();
+  int steps = 0, items = 0, sc = 0, eff = 0;
+  if (tid < ng && shape && gs[tid] < gs[tid + 1]) {
+    const int members = gs[tid + 1] - gs[tid];
+    int most = least[tid];
+    if (nlen[gs[tid]] < 0) {
+      most = 0;  // no row to read the prefix through (that row's length is reported)
+    } else if (shared < 0 || shared > most) {
+      bad = true;
+      most = 0;
+    }
+    eff = min(shared, most) / KT * KT;
+    int pairs, odd;
+    row_tiles(members, p, pairs, odd);
+    const int tiles = eff / KT;
+    items = tiles ? p.Hkv * pairs + odd * Hp : 0;
+    steps = items * (tiles + 1);
+    sc = tiles * ((members + p.nsc - 1) / p.nsc);
+  }
+  if (tid < ng) eff_of[tid] = eff;
+  int totS, totI, totC, totP;
+  const int s0 = prep_scan(steps, sh, &totS), i0 = prep_scan(items, sh, &totI), c0 = prep_scan(sc, sh, &totC);
+  if (tid < ng) {
+    m.gs[tid] = gs[tid];
+    m.eff[tid] = eff;
+    m.stepS[tid] = s0;
+    m.itemS[tid] = i0;
+    m.scS[tid] = c0;
+  }
+  // (eff_of is complete: the scans synchronised)
+  const int tiles = tid < B && n >= 0 ? (n - eff_of[grp] + KT - 1) / KT : 0;
+  const int cost = tiles > 0 ? tiles + 1 : 0;
+  const int p0 = prep_scan(cost, sh, &totP);
+  int totT;
+  const int t0 = prep_scan(tiles, sh, &totT);
+  if (tid < B) {
+    m.nlen[tid] = n;
+    m.grp[tid] = grp;
+    m.stepP[tid] = p0 * Hp;
+    m.scP[tid] = t0;
+  }
+  if (tid == 0) {
+    m.gs[ng] = B;
+    m.eff[ng] = 0;
+    m.stepS[ng] = totS;
+    m.itemS[ng] = totI;
+    m.scS[ng] = totC;
+    m.stepP[B] = totP * Hp;
+    m.scP[B] = totT;
+  }
+  if (bad || (!shape && tid == 0)) report(p.status, VG_ERR_DEVICE_BOUNDS);
 }
 
 // A contiguous run of key tiles of one item, as one CTA works on it.
@@ -205,21 +249,23 @@ struct Run {
   int item;           // index of its partials among the shared / private items
 };
 
-__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int x, int xend) {
+// The run at step x of a CTA that ends at xend; x moves past it (ntiles may be 0).
+__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int& x, int xend) {
   Run r;
   const int Hp = (p.Hkv + 1) / 2;
   const int totS = m.stepS[p.n_groups];
+  int off, len;  // step within the item, the item's steps
   if (x < totS) {
     const int g = find(m.stepS, p.n_groups, x);
-    const int tiles = m.eff[g] / KT;
+    const int members = m.gs[g + 1] - m.gs[g];
     int pairs, odd;
-    row_tiles(m.gs[g + 1] - m.gs[g], p.M, pairs, odd);
-    const int off = x - m.stepS[g];
-    const int it = off / tiles;
-    r.tile0 = off - it * tiles;
-    r.ntiles = min(tiles - r.tile0, xend - x);
+    row_tiles(members, p, pairs, odd);
+    len = m.eff[g] / KT + 1;
+    off = x - m.stepS[g];
+    const int it = off / len;
+    off -= it * len;
     r.row = r.seq0 = m.gs[g];
-    r.rows = (m.gs[g + 1] - m.gs[g]) * p.M;
+    r.rows = members * p.M;
     r.tok0 = 0;
     r.ntok = m.eff[g];
     r.priv = false;
@@ -228,24 +274,23 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     if (it < np) {
       r.mode = kPair;
       r.head[0] = r.head[1] = it / pairs;
-      r.r0[0] = (it - r.head[0] * pairs) * 2 * KT;
-      r.r0[1] = r.r0[0] + KT;
+      r.r0[0] = (it - r.head[0] * pairs) * 2 * p.RT;
+      r.r0[1] = r.r0[0] + p.RT;
     } else {
       const int hp = it - np;
       r.mode = 2 * hp + 1 < p.Hkv ? kHeads : kSingle;
       r.head[0] = 2 * hp;
       r.head[1] = 2 * hp + 1;
-      r.r0[0] = r.r0[1] = pairs * 2 * KT;
+      r.r0[0] = r.r0[1] = pairs * 2 * p.RT;
     }
   } else {
     const int y = x - totS;
     const int b = find(m.stepP, p.B, y);
     const int eff = m.eff[m.grp[b]];
-    const int tiles = (m.nlen[b] - eff + KT - 1) / KT;
-    const int off = y - m.stepP[b];
-    const int hp = off / tiles;
-    r.tile0 = off - hp * tiles;
-    r.ntiles = min(tiles - r.tile0, xend - x);
+    len = (m.nlen[b] - eff + KT - 1) / KT + 1;
+    off = y - m.stepP[b];
+    const int hp = off / len;
+    off -= hp * len;
     r.row = r.seq0 = b;
     r.rows = p.M;
     r.tok0 = eff;
@@ -257,16 +302,16 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     r.head[1] = 2 * hp + 1;
     r.r0[0] = r.r0[1] = 0;
   }
+  const int take = min(len - off, xend - x);  // the item's first step has no tile
+  r.tile0 = off > 0 ? off - 1 : 0;
+  r.ntiles = off + take - 1 - r.tile0;
+  x += take;
   return r;
 }
 
 // Ring order of a run's tiles (uses counted from the run's first): the order in which the MMA
 // issuer takes them.  Pair and single: K(0), then V(n), K(n + 1).  Heads: K0(0), K1(0), then
 // V0(n), K0(n + 1), V1(n), K1(n + 1).
-__device__ __forceinline__ int k_use(int mode, int w, int n) {
-  if (mode != kHeads) return 2 * n;
-  return n == 0 ? w : 4 * n - 1 + 2 * w;
-}
 __device__ __forceinline__ int v_use(int mode, int w, int n, int last) {
   if (mode != kHeads) return 2 * n + 1;
   return w == 0 ? 4 * n + 2 : (n < last ? 4 * n + 4 : 4 * n + 3);
@@ -279,9 +324,9 @@ struct SCfg {
   static constexpr int HALF_BYTES = KT * 128;     // 64 columns of a tile
   static constexpr int TILE_BYTES = KT * D * 2;   // a K or V tile, or a lane's Q
   static constexpr int OFF_RING = 2 * TILE_BYTES;
-  static constexpr int NBAR = 2 * kMaxSlots + 10;  // full, empty, then s_full, p_full, q_full, o_full [2], fin
+  static constexpr int NBAR = 2 * kMaxSlots + 14;  // full, empty, then s_full, p_full, q_full, o_full, q_empty, fin [2]
   static constexpr int TAIL = NBAR * 8 + 16;
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 20 * 32;
   static constexpr uint32_t TMEM_COLS = 512;      // S of the lanes at 0 and 128, O at 256 and 256 + D
   static constexpr uint32_t COL_O = 256;
   static int slots(int meta, size_t optin) {
@@ -294,37 +339,144 @@ struct SCfg {
   }
 };
 
-// 32 columns of this thread's tensor-memory lane; the caller waits (tc_wait_ld) before use.
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 64 columns of this thread's tensor-memory lane, loaded and waited for in one statement.
+__device__ __forceinline__ void tc_ld64_sync(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 // Bit patterns to 32 columns of this thread's lane.
 __device__ __forceinline__ void tc_st32b(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+// Named barrier of n threads that returns whether any of them brought `v`.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool v) {
+  uint32_t r;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+// tma_load_2d to a shared-memory address.
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                               uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+// 3-D tiled TMA load, as tma_load_2d_at.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// a * b + c on two fp32 values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The issuing forms below are run by a whole warp, convergent, so that their operands can stay in
+// uniform registers (in a branch of one thread each operand is moved there for each
+// instruction: 50 to 75 cycles an MMA instead of its 64); the instruction itself is predicated
+// on the elected thread.
+// D[tmem] (+)= A[smem] * B[smem]^T.
+__device__ __forceinline__ void tc_mma_one(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]: the A operand's rows are the lanes, two bf16 a column.
-__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ta_one(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
+// mbar_wait_ab for a whole warp, its tries suspended for up to 20 us each: a waiting warp that
+// polls takes issue slots from the softmax warps of its SM partition.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_ab(bar, parity, status, abort));
+  bool ok = false;
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(20000u)
+        : "memory");
+    if (__all_sync(0xffffffffu, done != 0)) return true;
+    if (*abort) break;
+    const unsigned long long t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      *abort = 1;
+      report(status, VG_ERR_DEVICE_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
+  return ok;
+}
+
+// Wait until use number (lap, slot) of a ring is filled.  A wait by parity is right only while
+// its barrier is at most one phase behind, and `full` alone does not ensure that here: with the
+// lanes taking turns, the slot's previous use may be the other lane's, and its copies may land
+// (or be read) later than those of a use this lane has already had.  So the previous use's
+// release is awaited first.  That wait is not ambiguous: the caller has had a use u' within
+// the last NS - 1 (rings have four slots or more); the producers fill in order, and to fill u' they had
+// seen everything up to u' - NS released, the slot's use of two laps ago among it.
+__device__ __forceinline__ bool filled(uint64_t* full, uint64_t* empty, int st, int lap, int32_t* status,
+                                       volatile int* abort) {
+  return (lap == 0 || warp_wait(&empty[st], (lap - 1) & 1, status, abort)) &&
+         warp_wait(&full[st], lap & 1, status, abort);
 }
 
 // Row (in the cache seen as rows of slots) of the TMA box that starts at token `tok` of
@@ -343,7 +495,7 @@ __device__ __forceinline__ int box_slot(const SharedParams& p, int row, int tok)
 template <int D>
 __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     shared_attn_kernel(const SharedParams p, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
   using C = SCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -355,7 +507,8 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
   uint64_t* p_full = s_full + 2;
   uint64_t* q_full = s_full + 4;
   uint64_t* o_full = s_full + 6;
-  uint64_t* fin = s_full + 8;
+  uint64_t* q_empty = s_full + 8;
+  uint64_t* fin = s_full + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + C::NBAR);
   // Raised by the first wait that runs out; every later wait then gives up at once.
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -365,238 +518,339 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
 
   if (threadIdx.x == 32) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 2);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 4);
-      mbar_init(&q_full[w], 4);
+      mbar_init(&p_full[w], 8);
+      mbar_init(&q_full[w], 1);
+      mbar_init(&q_empty[w], 1);
       mbar_init(&o_full[w], 1);
+      mbar_init(&fin[w], 1);
     }
-    mbar_init(fin, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tc_alloc(tmem_slot, C::TMEM_COLS);
+  if (warp == 17) tc_alloc(tmem_slot, C::TMEM_COLS);
   pdl_wait();
-  if (warp == 0) build_meta(p, m);
+  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += C::THREADS) mbase[i] = p.meta[i];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tmem_slot;
-  if (blockIdx.x == 0) {
-    const int n = meta_ints(p.B, p.n_groups);
-    for (int i = threadIdx.x; i < n; i += C::THREADS) p.meta[i] = mbase[i];
-  }
   pdl_launch_dependents();
 
   const int T = m.stepS[p.n_groups] + m.stepP[p.B];
   const int x0 = static_cast<int>(split_begin(blockIdx.x, T, p.nctas));
   const int x1 = static_cast<int>(split_begin(blockIdx.x + 1, T, p.nctas));
 
-  if (x0 < x1 && warp == 8) {
-    // ---------------------------------------------------------------- TMA producer
-    // A tile is 128 / box_rows boxes (page pieces) of 64 columns: one box a lane.
+  if (x0 < x1 && (warp == 16 || warp == 18)) {
+    // ---------------------------------------------------------------- TMA producers
+    // A tile is 128 / box_rows boxes (page pieces) of 64 columns: one box a lane, the boxes of
+    // every tile dealt out to two warps in turn (a warp issues its lanes' boxes one by one).
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
     const int BR = p.box_rows;
-    const int box = lane / C::HALVES, half = lane % C::HALVES;
+    const int e = 2 * lane + (warp == 18 ? 1 : 0);
+    const int box = e / C::HALVES;
     const bool has_box = box < KT / BR;
-    int u = 0;  // ring uses so far
+    const uint32_t ring0 = smem_u32(ring);
+    int off0 = 0;
+    int u = 0, st = 0, lap = 0;  // ring uses so far, slot and lap of the next one
     bool ok = true;
+    const bool leader = elect_one();
+    // a warp's boxes: one a lane, issued by one thread (an issue takes uniform operands: lanes
+    // issuing their own boxes would be run one by one with more work for each)
+    const int nb = KT / BR * C::HALVES, mine = (nb + (warp == 16 ? 1 : 0)) / 2;
+    auto load = [&](const CUtensorMap* map, int head, int y) {
+      if (lap > 0) ok = warp_wait(&empty[st], (lap - 1) & 1, p.status, abort);
+      if (!ok) return;
+      const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
+      if (leader) {
+        fence_proxy_async_smem();  // the slot may hold zeros written by the generic proxy
+        mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(have) * BR * 128));
+      }
+      for (int i = 0; i < mine; ++i) {
+        const int yi = __shfl_sync(0xffffffffu, y, i);
+        const int ei = 2 * i + (warp == 18 ? 1 : 0);
+        const int bi = ei / C::HALVES, hi = ei % C::HALVES;
+        if (leader && yi >= 0)
+          tma_load_2d_at(ring0 + st * C::TILE_BYTES + hi * C::HALF_BYTES + bi * BR * 128, map, head * D + hi * 64, yi,
+                         &full[st]);
+      }
+      __syncwarp();
+      ++u;
+      if (++st == NS) {
+        st = 0;
+        ++lap;
+      }
+    };
+    const int lw = warp == 18 ? 1 : 0;  // this warp brings the query tiles of that lane
+    uint32_t qpar = 1;                  // (the first wait passes)
     for (int x = x0; ok && x < x1;) {
       const Run r = make_run(p, m, x, x1);
-      x += r.ntiles;
-      // slot rows of this lane's box in tile n (-1: not loaded), looked up a tile ahead
-      auto lookup = [&](int n) {
-        const int at = (r.tile0 + n) * KT + box * BR;
-        return has_box && at < r.ntok ? box_slot(p, r.row, r.tok0 + at) : -1;
+      if (r.ntiles == 0) continue;
+      // page-table word of this lane's box in tile n, loaded a tile ahead; its slot row (-1: no
+      // box, or reported) when the tile is issued
+      auto word = [&](int n) {
+        const int tok = (r.tile0 + n) * KT + box * BR;
+        if (!has_box || n >= r.ntiles || tok >= r.ntok) return -1;
+        if (!p.ptab) return 0;
+        const int pi = (r.tok0 + tok) / p.psize;
+        return pi < p.pstride ? p.ptab[static_cast<size_t>(r.row) * p.pstride + pi] : -1;
       };
-      auto load = [&](const CUtensorMap* map, int head, int y) {
-        const int st = u % NS;
-        if (lane == 0 && u >= NS) ok = mbar_wait_ab(&empty[st], ((u / NS) - 1) & 1, p.status, abort);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, y >= 0));
-        if (lane == 0) {
-          fence_proxy_async_smem();  // the slot may hold zeros written by the generic proxy
-          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes * BR * 128));
+      auto slot_row = [&](int n, int w) {
+        const int tok = (r.tile0 + n) * KT + box * BR;
+        if (!has_box || n >= r.ntiles || tok >= r.ntok) return -1;
+        if (!p.ptab) return off0 + r.tok0 + tok;
+        if (w < 0 || (static_cast<int64_t>(w) + 1) * p.psize > p.capacity) {
+          report(p.status, VG_ERR_DEVICE_BOUNDS);
+          return -1;
+        }
+        return w * p.psize + (r.tok0 + tok) % p.psize;
+      };
+      off0 = p.ptab ? 0 : static_cast<int>(p.seq_offset[r.row]);
+      int w0 = word(0), w1 = word(1);
+      if (r.mode != kSingle || lw == 0) {
+        ok = warp_wait(&q_empty[lw], qpar, p.status, abort);
+        qpar ^= 1;
+        if (ok && leader) {
+          mbar_arrive_expect_tx(&q_full[lw], static_cast<uint32_t>(p.RT * 128 * C::HALVES));
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem_u32(smem) + lw * C::TILE_BYTES + h * C::HALF_BYTES, &tmQ, h * 64, r.head[lw] * p.G,
+                        r.seq0 * p.R + r.r0[lw] / p.G, &q_full[lw]);
         }
         __syncwarp();
-        if (y >= 0)
-          tma_load_2d(ring + static_cast<size_t>(st) * C::TILE_BYTES + half * C::HALF_BYTES + box * BR * 128, map,
-                      head * D + half * 64, y, &full[st]);
-        ++u;
-      };
-      int y = lookup(0);
-      load(&tmK, r.head[0], y);
+      }
+      int y = slot_row(0, w0);
+      if (ok) load(&tmK, r.head[0], y);
       if (ok && r.mode == kHeads) load(&tmK, r.head[1], y);
       for (int n = 0; ok && n < r.ntiles; ++n) {
         const bool more = n + 1 < r.ntiles;
-        const int yn = more ? lookup(n + 1) : -1;
+        const int w2 = word(n + 2);
         load(&tmV, r.head[0], y);
+        const int yn = slot_row(n + 1, w1);
         if (ok && more) load(&tmK, r.head[0], yn);
         if (r.mode == kHeads) {
           if (ok) load(&tmV, r.head[1], y);
           if (ok && more) load(&tmK, r.head[1], yn);
         }
         y = yn;
+        w1 = w2;
       }
     }
-    // no copy may still be in flight when the CTA exits (normally all were consumed)
-    if (lane == 0)
-      for (int i = u > NS ? u - NS : 0; i < u; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, p.status);
+    // No copy may still be in flight when the CTA exits: normally the issuers have waited
+    // for every one; after a lost wait the last ones issued here get 2 ms each to land.
+    if (!ok && lane == 0) {
+      volatile int never = 0;
+      for (int i = u > NS ? u - NS : 0; i < u; ++i)
+        mbar_wait_ab(&full[i % NS], (i / NS) & 1, nullptr, &never, 2000000ull);
+    }
     __syncwarp();
-  } else if (x0 < x1 && warp == 9 && lane == 0) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (x0 < x1 && (warp == 17 || warp == 19)) {
+    // ---------------------------------------------------------------- MMA issuers, one a lane
+    // The whole warp waits, one elected thread issues.  Descriptors are a base plus offsets in
+    // units of 16 bytes (addresses stay below 2^18, so the sums stay in the address field).
+    // A ring slot is free after two arrivals: one from each lane that reads it, or two from its
+    // only reader (see filled).  Where its lane has no tile (kSingle), lane 1 waits and arrives.
     constexpr uint32_t idS = tc_idesc_bf16(128, KT, 0, 0), idO = tc_idesc_bf16(128, D, 0, 1);
-    const uint32_t qbase = smem_u32(smem), rbase = smem_u32(ring);
-    int base = 0, nrun[2] = {0, 0}, np[2] = {0, 0};
-    bool ok = true;
-    auto wait_use = [&](int use) { return mbar_wait_ab(&full[use % NS], (use / NS) & 1, p.status, abort); };
+    const int w = __shfl_sync(0xffffffffu, warp == 19 ? 1 : 0, 0);
+    const uint64_t dq = tc_desc_sw128(smem_u32(smem) + w * C::TILE_BYTES, 16, 1024);
+    const uint64_t dk = tc_desc_sw128(smem_u32(ring), 16, 1024), dv = tc_desc_sw128(smem_u32(ring), C::HALF_BYTES, 1024);
+    const uint32_t ts = tm + w * 128, to = tm + C::COL_O + w * D;
+    const uint32_t lead = elect_one() ? 1u : 0u;
+    int st = 0, lap = 0;  // ring slot of the next use, its lap
+    uint32_t qpar = 0, ppar = 0;
+    bool ok = true, sole = false;  // sole: this lane is its slots' only reader
+    auto skip = [&](int n) {
+      st += n;
+      if (st >= NS) {
+        st -= NS;
+        ++lap;
+      }
+    };
+    auto release = [&] {
+      tc_commit_one(lead, &empty[st]);
+      if (sole) tc_commit_one(lead, &empty[st]);
+    };
+    // S = Q K^T from the next use (filled); end: Q has no further reader in this run
+    auto qk = [&](bool end) {
+      tc_fence_after();
+      const uint64_t db = dk + static_cast<uint64_t>(st * (C::TILE_BYTES / 16));
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        constexpr int H = C::HALF_BYTES / 16;
+        tc_mma_one(lead, ts, dq + (kk >> 2) * H + (kk & 3) * 2, db + (kk >> 2) * H + (kk & 3) * 2, idS,
+                   kk > 0 ? 1u : 0u);
+      }
+      tc_commit_one(lead, &s_full[w]);
+      release();
+      if (end) tc_commit_one(lead, &q_empty[w]);
+    };
+    // O (+)= P V from the next use (filled), P written
+    auto pv = [&](bool first, bool end) {
+      tc_fence_after();
+      const uint64_t db = dv + static_cast<uint64_t>(st * (C::TILE_BYTES / 16));
+#pragma unroll
+      for (int kk = 0; kk < KT / 16; ++kk)
+        tc_mma_ta_one(lead, to, ts + kk * 8, db + kk * 128, idO, (kk > 0 || !first) ? 1u : 0u);
+      release();
+      if (end) tc_commit_one(lead, &o_full[w]);
+    };
+    auto have = [&](int ahead) {  // the use `ahead` of the next one is filled
+      const int s2 = st + ahead < NS ? st + ahead : st + ahead - NS;
+      return filled(full, empty, s2, st + ahead < NS ? lap : lap + 1, p.status, abort);
+    };
     for (int x = x0; ok && x < x1;) {
       const Run r = make_run(p, m, x, x1);
-      x += r.ntiles;
-      const int lanes = r.mode == kSingle ? 1 : 2, last = r.ntiles - 1;
-      auto qk = [&](int w, int n) {
-        const int use = base + k_use(r.mode, w, n);
-        if (!(ok = ok && wait_use(use))) return;
-        tc_fence_after();
-        const uint32_t ka = rbase + (use % NS) * C::TILE_BYTES, qa = qbase + w * C::TILE_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(tm + w * 128, tc_desc_sw128(qa + (kk >> 2) * C::HALF_BYTES + (kk & 3) * 32, 16, 1024),
-                 tc_desc_sw128(ka + (kk >> 2) * C::HALF_BYTES + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
-        tc_commit(&s_full[w]);
-        if (r.mode != kPair || w == 1) tc_commit(&empty[use % NS]);
-      };
-      for (int w = 0; w < lanes; ++w) {
-        ok = ok && mbar_wait_ab(&q_full[w], nrun[w]++ & 1, p.status, abort);
-        qk(w, 0);
-      }
-      for (int n = 0; ok && n < r.ntiles; ++n) {
-        for (int w = 0; ok && w < lanes; ++w) {
-          const int use = base + v_use(r.mode, w, n, last);
-          ok = mbar_wait_ab(&p_full[w], np[w]++ & 1, p.status, abort) && wait_use(use);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = rbase + (use % NS) * C::TILE_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            tc_mma_ta(tm + C::COL_O + w * D, tm + w * 128 + kk * 8,
-                      tc_desc_sw128(va + kk * 2048, C::HALF_BYTES, 1024), idO, (n > 0 || kk > 0) ? 1u : 0u);
-          if (r.mode != kPair || w == 1) tc_commit(&empty[use % NS]);
-          if (n == last) tc_commit(&o_full[w]);
-          else qk(w, n + 1);
+      const int ntiles = __shfl_sync(0xffffffffu, r.ntiles, 0), mode = __shfl_sync(0xffffffffu, r.mode, 0);
+      if (ntiles == 0) continue;
+      const int last = ntiles - 1;
+      if (mode == kSingle && w == 1) {
+        for (int i = 0; ok && i < 2 * ntiles; ++i) {
+          ok = filled(full, empty, st, lap, p.status, abort);
+          if (lane == 0) mbar_arrive(&empty[st]);
+          skip(1);
         }
+        continue;
       }
-      base += run_uses(r.mode, r.ntiles);
+      // uses of a heads run: K0(0) K1(0), then V0(n) K0(n + 1) V1(n) K1(n + 1); else K(0), then
+      // V(n) K(n + 1)
+      sole = mode == kHeads;
+      ok = warp_wait(&q_full[w], qpar, p.status, abort);
+      qpar ^= 1;
+      if (sole) skip(w);
+      if (!(ok = ok && have(0))) break;
+      qk(last == 0);
+      skip(sole ? 2 - w : 1);
+      for (int n = 0; n <= last; ++n) {
+        const bool end = n == last;
+        const int theirs = sole ? (end ? 1 : 2) : 0;
+        if (w) skip(theirs);
+        // V(n) and K(n + 1) are awaited before P, whose arrival is what the products wait for
+        ok = have(0) && (end || have(1)) && warp_wait(&p_full[w], ppar, p.status, abort);
+        if (!ok) break;
+        ppar ^= 1;
+        pv(n == 0, end);
+        skip(1);
+        if (!end) {
+          qk(n + 1 == last);
+          skip(1);
+        }
+        if (!w) skip(theirs);
+      }
     }
-    tc_commit(fin);  // every MMA of this thread complete before the CTA tears down
-    mbar_wait(fin, 0, p.status);
-  } else if (x0 < x1 && warp < 8) {
+    tc_commit_one(lead, &fin[w]);  // every MMA of this thread complete before the CTA tears down
+    warp_wait(&fin[w], 0, p.status, abort);
+  } else if (x0 < x1 && warp < 16) {
     // ---------------------------------------------------------------- softmax lanes
-    const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-    const uint32_t ts = tm + (static_cast<uint32_t>(32 * quad) << 16) + w * 128;
-    const uint32_t to = tm + (static_cast<uint32_t>(32 * quad) << 16) + C::COL_O + w * D;
+    // Two threads a row: half 0 takes keys 0 .. 63 of each tile, half 1 the others, and each half
+    // of the output's columns where those are touched.  They use one running maximum, the row's
+    // maximum at the last time it was raised: while no key exceeds it by more than the slack, a
+    // thread needs nothing of the other but the word that this holds for both (which the
+    // barrier that lets P overwrite S brings along), and the maximum is off the path from S to P.
+    constexpr int HK = KT / 2;
+    const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = 32 * quad + lane;
+    const int pair_bar = 1 + 4 * w + quad;  // named barrier of the two warps that share rows
+    const uint32_t tq = tm + (static_cast<uint32_t>(32 * quad) << 16);
+    const uint32_t ts = tq + w * 128, to = tq + C::COL_O + w * D + half * (D / 2);
     const float c2 = p.scale_log2;
-    uint8_t* sQ = smem + w * C::TILE_BYTES;
     int base = 0, ns = 0, nr = 0;  // ring uses, tiles and runs of this lane so far
     for (int x = x0; x < x1;) {
       const Run r = make_run(p, m, x, x1);
-      x += r.ntiles;
+      if (r.ntiles == 0) continue;
       if (r.mode == kSingle && w == 1) {
         base += run_uses(r.mode, r.ntiles);
         continue;
       }
-      const int g = r.head[w], last = r.ntiles - 1;
-      const int nrows = min(KT, r.rows - r.r0[w]);
-      // query rows: row i of the unit is (member and verify row i / G, head i % G)
-      for (int e = lane; e < 32 * (D / 8); e += 32) {
-        const int i = quad * 32 + e / (D / 8), c = e % (D / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (i < nrows) {
-          const int rr = r.r0[w] + i;
-          const int bt = rr / p.G, hh = rr - bt * p.G;
-          v = *reinterpret_cast<const uint4*>(
-              p.q + ((static_cast<size_t>(r.seq0) * p.R + bt) * p.Hq + g * p.G + hh) * D + c * 8);
-        }
-        *reinterpret_cast<uint4*>(sQ + (c >> 3) * C::HALF_BYTES + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[w]);
-
-      float mx = neg_inf(), l = 0.f;
+      const int last = r.ntiles - 1;
+      const int nrows = min(p.RT, r.rows - r.r0[w]);
+      const bool live = 32 * quad < nrows;  // (a warp without rows only keeps the barriers' count)
+      float mx = neg_inf(), l = 0.f;        // the maximum in use (log2 units), this half's sum
       for (int n = 0; n < r.ntiles; ++n) {
-        const int valid = r.ntok - (r.tile0 + n) * KT;  // keys of the tile (128 or more: all)
+        const int left = r.ntok - (r.tile0 + n) * KT;  // keys of the tile (128 or more: all)
         warp_wait(&s_full[w], ns & 1, p.status, abort);
         ++ns;
         tc_fence_after();
-        if (valid < KT) {
-          // value rows past the range hold whatever was there: zeroed, so that 0 * V is 0.  (After
-          // the wait for S: by then the issuer has seen the slot's previous use filled, so this
-          // wait's parity is not that of an older phase.)
+        if (left < KT) {
+          // value rows past the range hold whatever was there: zeroed, so that 0 * V is 0 (after
+          // the wait for S, which orders this tile's V within NS uses of its K: see filled)
           const int use = base + v_use(r.mode, w, n, last);
-          warp_wait(&full[use % NS], (use / NS) & 1, p.status, abort);
+          filled(full, empty, use % NS, use / NS, p.status, abort);
           uint8_t* vt = ring + static_cast<size_t>(use % NS) * C::TILE_BYTES;
-          for (int e = quad * 32 + lane; e < C::HALVES * KT * 8; e += 128) {
+          for (int e = threadIdx.x & 255; e < C::HALVES * KT * 8; e += 256) {
             const int h = e / (KT * 8), i = (e >> 3) & (KT - 1);
-            if (i >= valid)
+            if (i >= left)
               *reinterpret_cast<uint4*>(vt + h * C::HALF_BYTES + i * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc_ld32(ts + 32 * c, s[c]);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        float t = neg_inf();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            asm volatile("" : "+r"(s[c][k]));  // (no use before the wait)
-            if (valid < KT && 32 * c + k >= valid) s[c][k] = 0xff800000u;
-            t = fmaxf(t, __uint_as_float(s[c][k]));
-          }
-        t *= c2;
-        const bool first = n == 0;
-        const float mn = first || t > mx + kRescaleSlack ? fmaxf(mx, t) : mx;
-        const bool resc = !first && mn != mx;
-        if (__any_sync(0xffffffffu, resc)) {
-          // rare: the running max rises (P V of the lane's previous tile has completed: the
-          // commit that brought this S came after it)
-          const float alpha = resc ? ex2(mx - mn) : 1.f;
-          l *= alpha;
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tc_ld32_sync(to + c0, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-            tc_st32(to + c0, o);
-          }
+        if (!live) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[w]);
+          continue;
         }
-        mx = mn;
-        float ls = 0.f;
+        const int valid = left - HK * half;  // keys of this half (64 or more: all)
+        uint32_t pk[HK / 2];
+        float ls;
+        for (bool known = n > 0;; known = true) {
+          if (known) {
+            // P = 2^(s c2 - mx) of this half, its sum (of the fp32 values: a packed add) and maximum
+            float s[HK];
+            tc_ld64_sync(ts + HK * half, s);
+            if (valid < HK) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+              for (int k = 0; k < HK; ++k)
+                if (k >= valid) s[k] = neg_inf();
+            }
+            float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float t2[2] = {s[0], s[1]};
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            const uint32_t a = s[2 * h + (k >> 5)][k & 31], b = s[2 * h + (k >> 5)][(k & 31) + 1];
-            // the sum takes the bf16 values that P V multiplies: a row's weights sum to one up
-            // to fp32 rounding, and what bf16 leaves off a dominant weight cancels
-            pk[k / 2] = pack_bf16(ex2(fmaf(__uint_as_float(a), c2, -mx)), ex2(fmaf(__uint_as_float(b), c2, -mx)));
-            ls = add_bf16x2_f32(pk[k / 2], ls);
+            for (int k = 0; k < HK; k += 2) {
+              t2[(k >> 1) & 1] = max3(t2[(k >> 1) & 1], s[k], s[k + 1]);
+              const float2 e = fma2(make_float2(s[k], s[k + 1]), make_float2(c2, c2), make_float2(-mx, -mx));
+              const float2 w2 = make_float2(ex2(e.x), ex2(e.y));
+              a2[(k >> 1) & 1] = add2(a2[(k >> 1) & 1], w2);
+              pk[k / 2] = pack_bf16(w2.x, w2.y);
+            }
+            ls = (a2[0].x + a2[0].y) + (a2[1].x + a2[1].y);
+            // (both threads of each row have read S after the barrier: P may overwrite it)
+            if (!named_bar_or(pair_bar, 64, row < nrows && fmaxf(t2[0], t2[1]) * c2 > mx + kRescaleSlack)) break;
           }
-          tc_st32b(ts + 32 * h, pk);
+          // rare, and each run's first tile: the row's maximum over the whole tile, which both
+          // threads of the row read for themselves, becomes the one in use; then (again) P
+          float t = neg_inf();
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT; c0 += 32) {
+            float v[32];
+            tc_ld32_sync(ts + c0, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) t = fmaxf(t, c0 + k < left ? v[k] : neg_inf());
+          }
+          t *= c2;
+          const float mn = n == 0 || t > mx + kRescaleSlack ? fmaxf(mx, t) : mx;
+          if (n > 0) {
+            // (P V of the lane's previous tile has completed: the commit that brought this S
+            // came after it)
+            const float alpha = mn != mx ? ex2(mx - mn) : 1.f;
+            l *= alpha;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 2; c0 += 32) {
+              float o[32];
+              tc_ld32_sync(to + c0, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tc_st32(to + c0, o);
+            }
+          }
+          mx = mn;
         }
         l += ls;
+        tc_st32b(ts + (HK / 2) * half, pk);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -606,22 +860,28 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       warp_wait(&o_full[w], nr & 1, p.status, abort);
       ++nr;
       tc_fence_after();
-      const size_t prow =
-          r.priv ? (static_cast<size_t>(blockIdx.x + r.item) * 2 + w) * p.Mpad + row
-                 : (static_cast<size_t>(blockIdx.x + r.item) * 2 + w) * KT + row;
-      float* po = (r.priv ? p.partp_o : p.parts_o) + prow * D;
-      if (32 * quad < nrows) {
+      if (live) {
+        // four columns of 32 rows lie together: a warp's stores are 512 contiguous bytes
+        const int height = r.priv ? p.Mpad : KT;
+        const size_t unit = static_cast<size_t>(blockIdx.x + r.item) * 2 + w;
+        float* po = (r.priv ? p.partp_o : p.parts_o) + (unit * D + half * (D / 2)) * height + row * 4;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
           float o[32];
           tc_ld32_sync(to + c0, o);
           if (row < nrows) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(po + c0 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              *reinterpret_cast<float4*>(po + static_cast<size_t>(c0 + k) * height) =
+                  make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           }
         }
-        if (row < nrows) *reinterpret_cast<float2*>((r.priv ? p.partp_ml : p.parts_ml) + prow * 2) = make_float2(mx, l);
+        // (max, sum of each half of the keys, unused)
+        float* pml = (r.priv ? p.partp_ml : p.parts_ml) + (unit * height + row) * 4;
+        if (row < nrows) {
+          if (half == 0) *reinterpret_cast<float2*>(pml) = make_float2(mx, l);
+          else pml[2] = l;
+        }
       }
       tc_fence_before();
       base += run_uses(r.mode, r.ntiles);
@@ -630,36 +890,41 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tc_dealloc(tm, C::TMEM_COLS);
   }
 }
 
 // ---------------------------------------------------------------- combine
-// One warp per output row, lanes across d: the partials of the row's shared item by CTA, of
-// its private item by CTA, then its causal keys u = 0 .. t: a fixed order.
-constexpr int kCombWarps = 8;
+// A CTA merges eight consecutive rows of a (sequence, KV head).  First a warp a row: the
+// causal logits of the row's own keys u = 0 .. t, the maximum and the sum over those and the
+// row's partials (lanes across partials).  Then a thread a (row, four columns): the partials
+// of the row's shared item by CTA, of its private item by CTA, then the causal values: a fixed
+// order.
+constexpr int kCombRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kCombWarps * 32) shared_combine_kernel(const SharedParams p) {
-  constexpr int PER = D / 32;
-  __shared__ float lgs[kCombWarps][16];
+__global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParams p) {
+  constexpr int PER = D / 32, WARPS = D / 16, CH = D / 8;
+  __shared__ float lgs[kCombRows][16], rowM[kCombRows], rowL[kCombRows];
+  __shared__ int seg[kCombRows][4];        // first CTA and count of the row's shared, private partials
+  __shared__ size_t at[kCombRows][2];      // unit row of the first of each
   __shared__ __align__(16) __nv_bfloat16 kvs[2][16][D];
   pdl_launch_dependents();
   pdl_wait();
   const Meta m = meta_at(p.meta, p.B, p.n_groups);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rblocks = (p.M + kCombWarps - 1) / kCombWarps;
-  const int bg = blockIdx.x / rblocks, r0 = (blockIdx.x - bg * rblocks) * kCombWarps;
-  const int r = r0 + warp, g = bg % p.Hkv, b = bg / p.Hkv;
-  const int n = m.nlen[b];
+  const int rblocks = (p.M + kCombRows - 1) / kCombRows;
+  const int bg = blockIdx.x / rblocks, r0 = (blockIdx.x - bg * rblocks) * kCombRows;
+  const int g = bg % p.Hkv, b = bg / p.Hkv;
+  const int n = m.nlen[b], grp = m.grp[b], eff = m.eff[grp], gs0 = m.gs[grp], gs1 = m.gs[grp + 1];
+  const int stepS = m.stepS[grp], itemS = m.itemS[grp], totS = m.stepS[p.n_groups], stepP = m.stepP[b];
+  const int T = totS + m.stepP[p.B];
   if (n < 0) return;  // the whole CTA
-  const bool active = r < p.M;
-  const int t = active ? r / p.G : 0, jh = r - t * p.G;
-  const int tmax = min(p.M - 1, r0 + kCombWarps - 1) / p.G;
-  constexpr int CH = D / 8;
-  for (int e = tid; e < 2 * (tmax + 1) * CH; e += kCombWarps * 32) {
+  const int rows = min(kCombRows, p.M - r0);
+  const int tmax = (r0 + rows - 1) / p.G;
+  for (int e = tid; e < 2 * (tmax + 1) * CH; e += 2 * D) {
     const int which = e / ((tmax + 1) * CH), rem = e - which * (tmax + 1) * CH;
     const int u = rem / CH, c = rem - u * CH;
     const __nv_bfloat16* fresh = which ? p.v_new : p.k_new;
@@ -673,140 +938,144 @@ __global__ void __launch_bounds__(kCombWarps * 32) shared_combine_kernel(const S
     reinterpret_cast<uint4*>(&kvs[which][u][0])[c] =
         src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
   }
-  // where the row's partials are: shared ones from CTA cs on, private ones from CTA cp on
-  const int grp = m.grp[b], Hp = (p.Hkv + 1) / 2;
-  const int totS = m.stepS[p.n_groups];
-  const int T = totS + m.stepP[p.B];
-  int cs = 0, nS = 0, cp = 0, nP = 0;
-  size_t baseS = 0, strideS = 2 * KT, baseP = 0;
-  if (active) {
-    const int tiles = m.eff[grp] / KT;
+  __syncthreads();
+  for (int rl = warp; rl < rows; rl += WARPS) {
+    const int r = r0 + rl, t = r / p.G, jh = r - t * p.G;
+    // where the row's partials are: an item's tiles are its steps but the first, and a CTA that
+    // owns one of those left a partial
+    int cs = 0, nS = 0, cp = 0, nP = 0;
+    size_t baseS = 0, baseP = 0;
+    const int tiles = eff / KT, ptiles = (n - eff + KT - 1) / KT;
     if (tiles > 0) {
       int pairs, odd;
-      row_tiles(m.gs[grp + 1] - m.gs[grp], p.M, pairs, odd);
-      const int rr = (b - m.gs[grp]) * p.M + r, rt = rr / KT;
-      int it, w;
-      if ((rt >> 1) < pairs) {
-        it = g * pairs + (rt >> 1);
-        w = rt & 1;
-      } else {
-        it = p.Hkv * pairs + (g >> 1);
-        w = g & 1;
-      }
-      const int s0 = m.stepS[grp] + it * tiles;
-      cs = static_cast<int>(owner_cta(s0, T, p.nctas));
-      nS = static_cast<int>(owner_cta(s0 + tiles - 1, T, p.nctas)) - cs + 1;
-      baseS = (static_cast<size_t>(cs + m.itemS[grp] + it) * 2 + w) * KT + (rr - rt * KT);
+      row_tiles(gs1 - gs0, p, pairs, odd);
+      const int rr = (b - gs0) * p.M + r, rt = rr / p.RT;
+      const bool pair = (rt >> 1) < pairs;
+      const int it = pair ? g * pairs + (rt >> 1) : p.Hkv * pairs + (g >> 1), w = pair ? rt & 1 : g & 1;
+      const int s0 = stepS + it * (tiles + 1);
+      cs = static_cast<int>(owner_cta(s0 + 1, T, p.nctas));
+      nS = static_cast<int>(owner_cta(s0 + tiles, T, p.nctas)) - cs + 1;
+      baseS = (static_cast<size_t>(cs + itemS + it) * 2 + w) * KT * D + static_cast<size_t>(rr - rt * p.RT);
     }
-    const int ptiles = (n - m.eff[grp] + KT - 1) / KT;
     if (ptiles > 0) {
-      const int s0 = totS + m.stepP[b] + (g >> 1) * ptiles;
-      cp = static_cast<int>(owner_cta(s0, T, p.nctas));
-      nP = static_cast<int>(owner_cta(s0 + ptiles - 1, T, p.nctas)) - cp + 1;
-      baseP = (static_cast<size_t>(cp + b * Hp + (g >> 1)) * 2 + (g & 1)) * p.Mpad + r;
+      const int Hp = (p.Hkv + 1) / 2;
+      const int s0 = totS + stepP + (g >> 1) * (ptiles + 1);
+      cp = static_cast<int>(owner_cta(s0 + 1, T, p.nctas));
+      nP = static_cast<int>(owner_cta(s0 + ptiles, T, p.nctas)) - cp + 1;
+      baseP = (static_cast<size_t>(cp + b * Hp + (g >> 1)) * 2 + (g & 1)) * p.Mpad * D + r;
     }
-  }
-  const int nseg = nS + nP;
-  // (a CTA between the first and the last has steps of the item: T >= nctas there, or it is
-  // skipped as empty)
-  auto nonempty = [&](int i) { return split_nonempty(i < nS ? cs + i : cp + i - nS, T, p.nctas); };
-  auto prow = [&](int i) {
-    return i < nS ? baseS + static_cast<size_t>(i) * strideS : baseP + static_cast<size_t>(i - nS) * 2 * p.Mpad;
-  };
-  float qv[PER];
-  if (active) {
+    // (max, sum) of partial i; a CTA without steps wrote none
+    auto load_ml = [&](int i, float& ms, float& ls) {
+      ms = neg_inf();
+      ls = 0.f;
+      if (i >= nS + nP || !split_nonempty(i < nS ? cs + i : cp + i - nS, T, p.nctas)) return;
+      const float* src =
+          i < nS ? p.parts_ml + ((baseS / (KT * D) + 2 * static_cast<size_t>(i)) * KT + baseS % (KT * D)) * 4
+                 : p.partp_ml + ((baseP / (static_cast<size_t>(p.Mpad) * D) + 2 * static_cast<size_t>(i - nS)) * p.Mpad + r) * 4;
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      ms = v.x;
+      ls = v.y + v.z;
+    };
+    float pm, pl;
+    load_ml(lane, pm, pl);
+    float qv[PER];
     const __nv_bfloat16* qrow = p.q + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; ++e) qv[e] = __bfloat162float(qrow[e]);
+    float M = neg_inf();
+    for (int u = 0; u <= t; ++u) {
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc += qv[e] * __bfloat162float(kvs[0][u][lane * PER + e]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      acc *= p.scale_log2;
+      M = fmaxf(M, acc);
+      if (lane == 0) lgs[rl][u] = acc;
+    }
+    float pmax = pm;
+    for (int i = 32; i < nS + nP; i += 32) {
+      float ms, ls;
+      load_ml(i + lane, ms, ls);
+      pmax = fmaxf(pmax, ms);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
+    M = fmaxf(M, pmax);
+    float l = pm != neg_inf() ? ex2(pm - M) * pl : 0.f;
+    for (int i = 32; i < nS + nP; i += 32) {
+      float ms, ls;
+      load_ml(i + lane, ms, ls);
+      if (ms != neg_inf()) l += ex2(ms - M) * ls;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    __syncwarp();
+    for (int u = 0; u <= t; ++u) l += ex2(lgs[rl][u] - M);
+    if (lane == 0) {
+      rowM[rl] = M;
+      rowL[rl] = l;
+      seg[rl][0] = cs;
+      seg[rl][1] = nS;
+      seg[rl][2] = cp;
+      seg[rl][3] = nP;
+      at[rl][0] = baseS;
+      at[rl][1] = baseP;
+    }
   }
   __syncthreads();
-  if (!active) return;
-  float* lg = lgs[warp];
-  float M = neg_inf();
-  for (int u = 0; u <= t; ++u) {
-    float acc = 0.f;
+  const int rl = tid & (kCombRows - 1), c = tid / kCombRows;  // row, group of four columns
+  if (rl >= rows) return;
+  const int r = r0 + rl, t = r / p.G, jh = r - t * p.G;
+  const float M = rowM[rl];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc += qv[e] * __bfloat162float(kvs[0][u][lane * PER + e]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    acc *= p.scale_log2;
-    M = fmaxf(M, acc);
-    if (lane == 0) lg[u] = acc;
-  }
-  __syncwarp();
-  auto load_ml = [&](int i, float& ms, float& ls) {
-    ms = neg_inf();
-    ls = 0.f;
-    if (i < nseg && nonempty(i)) {
-      const float2 v = *reinterpret_cast<const float2*>((i < nS ? p.parts_ml : p.partp_ml) + prow(i) * 2);
-      ms = v.x;
-      ls = v.y;
-    }
-  };
-  float pm, pl;
-  load_ml(lane, pm, pl);
-  float pmax = pm;
-  for (int s0 = 32; s0 < nseg; s0 += 32) {
-    float ms, ls;
-    load_ml(s0 + lane, ms, ls);
-    pmax = fmaxf(pmax, ms);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
-  M = fmaxf(M, pmax);
-  float acc[PER] = {}, l = 0.f;
-  for (int s0 = 0; s0 < nseg; s0 += 32) {
-    float ms = pm, ls = pl;
-    if (s0 > 0) load_ml(s0 + lane, ms, ls);
-    const float wgt = ms != neg_inf() ? ex2(ms - M) : 0.f;
-    float wl = wgt * ls;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
-    l += wl;
-    const int cnt = min(32, nseg - s0);
-    for (int q0 = 0; q0 < cnt; q0 += 4) {
-      float v[4][PER];
+  for (int part = 0; part < 2; ++part) {
+    const int c0 = seg[rl][2 * part], cnt = seg[rl][2 * part + 1];
+    const size_t height = part ? p.Mpad : KT, unit = height * D;
+    const size_t first = at[rl][part], row = first % unit;
+    const float* po = (part ? p.partp_o : p.parts_o) + (first - row) + row * 4 + static_cast<size_t>(c) * height * 4;
+    const float* pml = (part ? p.partp_ml : p.parts_ml) + (first / unit * height + row) * 4;
+    for (int i0 = 0; i0 < cnt; i0 += 4) {
+      float ml[4];
+      float4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = s0 + q0 + q;
-        const bool have = i < nseg && nonempty(i);
-        const float* src = (i < nS ? p.parts_o : p.partp_o) + (have ? prow(i) : 0) * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-          const float2 x = have ? *reinterpret_cast<const float2*>(src + e) : make_float2(0.f, 0.f);
-          v[q][e] = x.x;
-          v[q][e + 1] = x.y;
+        const int i = i0 + q;
+        ml[q] = neg_inf();
+        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < cnt && split_nonempty(c0 + i, T, p.nctas)) {
+          ml[q] = pml[static_cast<size_t>(i) * 8 * height];
+          v[q] = *reinterpret_cast<const float4*>(po + static_cast<size_t>(i) * 2 * unit);
         }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, wgt, (q0 + q) & 31);
-        if (q0 + q < cnt) {
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] += wq * v[q][e];
-        }
+        const float w = ml[q] != neg_inf() ? ex2(ml[q] - M) : 0.f;
+        acc.x += w * v[q].x;
+        acc.y += w * v[q].y;
+        acc.z += w * v[q].z;
+        acc.w += w * v[q].w;
       }
     }
   }
   for (int u = 0; u <= t; ++u) {
-    const float wu = ex2(lg[u] - M);
-    l += wu;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] += wu * __bfloat162float(kvs[1][u][lane * PER + e]);
+    const float w = ex2(lgs[rl][u] - M);
+    const __nv_bfloat16* v = &kvs[1][u][4 * c];
+    acc.x += w * __bfloat162float(v[0]);
+    acc.y += w * __bfloat162float(v[1]);
+    acc.z += w * __bfloat162float(v[2]);
+    acc.w += w * __bfloat162float(v[3]);
   }
-  const float inv = 1.f / l;
-  __nv_bfloat16* o = p.out + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + lane * PER;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = __float2bfloat16_rn(acc[e] * inv);
+  const float inv = 1.f / rowL[rl];
+  *reinterpret_cast<uint2*>(p.out + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + 4 * c) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   if (p.k_new && jh == 0) {  // append verify row t
     const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + t);
     if (slot >= 0) {
-      const size_t dst = (slot * p.Hkv + g) * D + lane * PER;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        p.K[dst + e] = kvs[0][t][lane * PER + e];
-        p.V[dst + e] = kvs[1][t][lane * PER + e];
-      }
+      const size_t dst = (slot * p.Hkv + g) * D + 4 * c;
+      *reinterpret_cast<uint2*>(p.K + dst) = *reinterpret_cast<const uint2*>(&kvs[0][t][4 * c]);
+      *reinterpret_cast<uint2*>(p.V + dst) = *reinterpret_cast<const uint2*>(&kvs[1][t][4 * c]);
     }
   }
 }
@@ -814,28 +1083,8 @@ __global__ void __launch_bounds__(kCombWarps * 32) shared_combine_kernel(const S
 // ---------------------------------------------------------------- scores
 // scores[b][i] = scale * sum over the mask's rows and all heads of q . K_i = scale * sum over
 // KV heads g of Q_b,g . K_i,g with Q_b,g the sum of the sequence's masked query rows of head g.
-// Q is fp32; it enters the tensor cores as three bf16 parts whose sum is Q to 2^-24.
-__global__ void __launch_bounds__(128) shared_qsum_kernel(const SharedParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv, d = threadIdx.x;
-  if (d >= p.D) return;
-  float acc = 0.f;
-  for (uint32_t bits = p.mask; bits != 0u; bits &= bits - 1u) {
-    const int t = __ffs(bits) - 1;
-    const __nv_bfloat16* src = p.q + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G) * p.D + d;
-    for (int h = 0; h < p.G; ++h) acc += __bfloat162float(src[h * p.D]);
-  }
-  const size_t width = static_cast<size_t>(p.Hkv) * p.D, part = static_cast<size_t>(p.Bpad) * width;
-  __nv_bfloat16* dst = p.qsum + b * width + g * p.D + d;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(acc);
-    dst[k * part] = h;
-    acc -= __bfloat162float(h);
-  }
-}
-
+// Q is fp32 and enters the tensor cores as three bf16 parts.
+//
 // One item is a tile of 128 keys and up to N members: S^T[keys][members] on the tensor cores
 // (the keys are the M rows, so few members cost little), one KV head at a time into a double
 // buffer; four warps add the heads' tiles in fp32 registers (the tensor core's own sum runs
@@ -886,7 +1135,7 @@ __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
   }
   if (warp == 5) tc_alloc(tmem_slot, C::TMEM_COLS);
   pdl_wait();
-  if (warp == 0) build_meta(p, m);
+  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += C::THREADS) mbase[i] = p.meta[i];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1047,16 +1296,16 @@ cudaError_t launch_scores(const SharedParams& p, const CUtensorMap& tmK, const C
   const size_t smem = C::smem(meta_ints(p.B, p.n_groups));
   cudaError_t e = ensure_smem<shared_score_kernel<D, N>>(smem);
   if (e != cudaSuccess) return e;
-  Launch q(p.B * p.Hkv, 128, 0, stream);
-  if ((e = cudaLaunchKernelEx(&q.cfg, shared_qsum_kernel, p)) != cudaSuccess) return e;
   Launch z(p.nctas, C::THREADS, smem, stream);
   return cudaLaunchKernelEx(&z.cfg, shared_score_kernel<D, N>, p, tmK, tmZ);
 }
 
 template <int D>
 cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                            const CUtensorMap& tmZ, cudaStream_t stream) {
+                            const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream) {
   cudaError_t e;
+  Launch f(p.mask ? 1 + p.B : 1, kPrepThreads, 0, stream);
+  if ((e = cudaLaunchKernelEx(&f.cfg, shared_prep_kernel, p)) != cudaSuccess) return e;
   if (p.mask) {
     e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, stream) : launch_scores<D, 64>(p, tmK, tmZ, stream);
     if (e != cudaSuccess) return e;
@@ -1065,8 +1314,8 @@ cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const
   const size_t smem = C::smem(p.nslots, meta_ints(p.B, p.n_groups));
   if ((e = ensure_smem<shared_attn_kernel<D>>(smem)) != cudaSuccess) return e;
   Launch a(p.nctas, C::THREADS, smem, stream);
-  if ((e = cudaLaunchKernelEx(&a.cfg, shared_attn_kernel<D>, p, tmK, tmV)) != cudaSuccess) return e;
-  Launch c(p.B * p.Hkv * ((p.M + kCombWarps - 1) / kCombWarps), kCombWarps * 32, 0, stream);
+  if ((e = cudaLaunchKernelEx(&a.cfg, shared_attn_kernel<D>, p, tmK, tmV, tmQ)) != cudaSuccess) return e;
+  Launch c(p.B * p.Hkv * ((p.M + kCombRows - 1) / kCombRows), 2 * D, 0, stream);
   return cudaLaunchKernelEx(&c.cfg, shared_combine_kernel<D>, p);
 }
 
@@ -1080,8 +1329,9 @@ int shared_slots(int D, int B, int n_groups, size_t smem_optin) {
 }
 
 cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                          const CUtensorMap& tmZ, cudaStream_t stream) {
-  return p.D == 64 ? launch_shared_t<64>(p, tmK, tmV, tmZ, stream) : launch_shared_t<128>(p, tmK, tmV, tmZ, stream);
+                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream) {
+  return p.D == 64 ? launch_shared_t<64>(p, tmK, tmV, tmQ, tmZ, stream)
+                   : launch_shared_t<128>(p, tmK, tmV, tmQ, tmZ, stream);
 }
 
 }  // namespace vg

@@ -1201,6 +1201,27 @@ vg_status vg_pages_compact(const vg_page_pool* pool, const vg_kv_cache* caches, 
 namespace vg {
 namespace {
 
+// Query rows of a row tile: whole groups of G heads.
+int shared_row_tile(int G) { return kSharedTileKeys / G * G; }
+
+// q as a 3-D tensor [B * R][Hq][D]; a box is 64 columns of the G heads of 128 / G rows, which
+// lands in shared memory as consecutive rows of 128 bytes (128-byte swizzle).
+vg_status encode_query_map(CUtensorMap* map, const void* q, const Shape& s) {
+  EncodeTiledFn enc;
+  const vg_status st = get_encoder(&enc);
+  if (st != VG_OK) return st;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.Hq),
+                              static_cast<cuuint64_t>(s.B) * s.R};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D) * 2, static_cast<cuuint64_t>(s.Hq) * s.D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(s.G), static_cast<cuuint32_t>(kSharedTileKeys / s.G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return VG_OK;
+}
+
 struct SharedWs {
   size_t meta, parts_o, parts_ml, partp_o, partp_ml, qsum, total;
   int64_t items;  // shared and private items at most
@@ -1209,9 +1230,10 @@ struct SharedWs {
 SharedWs shared_ws(const Shape& s, int n_groups, int sms) {
   SharedWs w = {};
   const int64_t rows = static_cast<int64_t>(s.B) * s.M, ng = n_groups, Hp = (s.Hkv + 1) / 2;
-  // pairs of row tiles over all groups: floor(ceil(rows_g / 128) / 2) each, which is at most
-  // (rows_g + 127) / 256, and nothing below 129 rows
-  const int64_t by_tile = (rows + 127 * ng) / 256, by_rows = rows / 129;
+  // pairs of row tiles (RT rows each) over all groups: floor(ceil(rows_g / RT) / 2) each, which
+  // is at most (rows_g + RT - 1) / (2 RT), and none without RT + 1 rows
+  const int64_t RT = shared_row_tile(s.G);
+  const int64_t by_tile = (rows + (RT - 1) * ng) / (2 * RT), by_rows = rows / (RT + 1);
   const int64_t pairs = by_tile < by_rows ? by_tile : by_rows;
   const int64_t shared = s.Hkv * pairs + Hp * (ng < s.B ? ng : s.B);
   const int64_t priv = s.B * Hp;
@@ -1226,9 +1248,9 @@ SharedWs shared_ws(const Shape& s, int n_groups, int sms) {
   const size_t prows = static_cast<size_t>(sms + priv) * 2 * s.Mpad;
   w.meta = take(static_cast<size_t>(shared_meta_ints(s.B, n_groups)) * 4);
   w.parts_o = take(srows * s.D * 4);
-  w.parts_ml = take(srows * 8);
+  w.parts_ml = take(srows * 16);
   w.partp_o = take(prows * s.D * 4);
-  w.partp_ml = take(prows * 8);
+  w.partp_ml = take(prows * 16);
   w.qsum = take(static_cast<size_t>(3) * ((s.B + 15) & ~15) * s.Hkv * s.D * 2);
   w.total = off;
   return w;
@@ -1276,7 +1298,7 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   DevInfo di;
   if ((st = device_info(&di)) != VG_OK) return st;
   const SharedWs w = shared_ws(s, groups->n_groups, di.sms);
-  if (w.items * (s.max_len / kSharedTileKeys + 1) > 0x7fffffffLL)
+  if (w.items * (s.max_len / kSharedTileKeys + 2) > 0x7fffffffLL)
     return fail(VG_ERR_UNSUPPORTED_SHAPE, "B=%d sequences of up to max_len=%d tokens are too many tiles", s.B, s.max_len);
   if (!ws) return fail(VG_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", w.total);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(VG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
@@ -1286,9 +1308,10 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   if (p.nslots < 4) return fail(VG_ERR_UNSUPPORTED_SHAPE, "too little shared memory for B=%d", s.B);
   p.Bpad = (s.B + 15) & ~15;
   p.qsum = at<__nv_bfloat16>(ws, w.qsum);
-  CUtensorMap tmK, tmV, tmZ;
+  CUtensorMap tmK, tmV, tmQ, tmZ;
   if ((st = encode_cache_map(&tmK, cache->K, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
   if ((st = encode_cache_map(&tmV, cache->V, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
+  if ((st = encode_query_map(&tmQ, q, s)) != VG_OK) return st;
   tmZ = tmK;
   if (row_mask && (st = encode_cache_map(&tmZ, p.qsum, 3 * p.Bpad, s.Hkv, s.D, 16)) != VG_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -1314,6 +1337,7 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   p.D = s.D;
   p.M = s.M;
   p.Mpad = s.Mpad;
+  p.RT = shared_row_tile(s.G);
   p.max_len = s.max_len;
   p.scale = s.scale;
   p.scale_log2 = s.scale * 1.4426950408889634f;
@@ -1329,7 +1353,7 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   p.score_stride = score_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.status = dev_status;
-  const cudaError_t e = launch_shared(p, tmK, tmV, tmZ, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_shared(p, tmK, tmV, tmQ, tmZ, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "shared verify launch");
   return VG_OK;
 }

@@ -133,6 +133,7 @@ struct SharedParams {
   const int32_t* shared_len;   // [n_groups]
   int n_groups;
   int B, Hq, Hkv, G, R, D, M, Mpad;  // M = G * R rows per (sequence, KV head), Mpad = 16 * ceil(M / 16)
+  int RT;                      // query rows of a row tile: the largest multiple of G up to 128
   int max_len;
   float scale, scale_log2;
   uint32_t mask;               // verify rows summed into scores (0: no scores)
@@ -141,10 +142,10 @@ struct SharedParams {
   int nctas, nslots;           // attention grid; ring slots of a CTA
   // workspace
   int32_t* meta;         // the batch's layout (shared_meta_ints)
-  float* parts_o;        // [nctas + shared items][2][128][D] unnormalised partial outputs
-  float* parts_ml;       // [...][2] (running max in log2 units, sum)
-  float* partp_o;        // [nctas + private items][2][Mpad][D]
-  float* partp_ml;
+  float* parts_o;        // [nctas + shared items][2][D / 4][128][4] unnormalised partial outputs
+  float* parts_ml;       // [nctas + shared items][2][128][4] max in use (log2 units), sums of both halves of the keys
+  float* partp_o;        // [nctas + private items][2][D / 4][Mpad][4]
+  float* partp_ml;       // [nctas + private items][2][Mpad][4]
   __nv_bfloat16* qsum;   // [3][Bpad][Hkv * D] the masked rows' summed queries, in three parts
   // outputs
   float* scores;         // [B][score_stride] or null
@@ -234,9 +235,10 @@ int accept_tiles(int V);   // tiles of the sampling draw over a row of V entries
 // Warps of the draft step's combine kernel (4, 8 or 16 from the most partials a
 // sequence has), or 0 when every sequence's entries sit in one CTA (no combine runs).
 int draft_combine_warps(int B, int slots, int nctas);
-// tmZ: qsum as rows of Hkv * D, boxes of 64 columns x 16 rows (unused without scores)
+// tmQ: q as [B * R][Hq][D], boxes of 64 columns x G heads x 128 / G rows; tmZ: qsum as rows of
+// Hkv * D, boxes of 64 columns x 16 rows (unused without scores)
 cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                          const CUtensorMap& tmZ, cudaStream_t stream);
+                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream);
 int shared_meta_ints(int B, int n_groups);
 int shared_slots(int D, int B, int n_groups, size_t smem_optin);  // ring slots that fit a CTA
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream);
