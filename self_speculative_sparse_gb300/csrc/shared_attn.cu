@@ -38,12 +38,18 @@ constexpr int kMaxSlots = 12;  // ring slots (K or V tiles) at most
 
 // ---------------------------------------------------------------- the batch's layout
 // Everything the kernels need about lengths and groups, in the workspace: built from the
-// device arrays by one CTA of a first small kernel, copied to shared memory by the others.
-// An item is one unit of rows (a pair of row tiles of a KV head, or one row tile of two KV
-// heads) and its whole key range.  The attention CTAs split the items' steps evenly, an item
-// counting one step more than its key tiles: filling and draining its pipeline costs a CTA
-// about as much as a tile, and without that step the CTAs at the short private ranges were
-// the last to finish.
+// device arrays by one CTA of a first small kernel, copied to shared memory by the others (built
+// by every CTA for itself it takes each kernel 4 us more).  An item is one unit of rows (a pair
+// of row tiles of a KV head, or one row tile of two KV heads) and its whole key range; it counts
+// one step more than its key tiles, since filling and draining its pipeline costs a CTA about as
+// much as a tile.
+//
+// The attention CTAs split the items' steps evenly.  If any group has pairs of row tiles, the
+// shared items are bound by the tensor cores and the private ones by reading keys and values
+// that one sequence's few rows use once: then the two kinds are split separately, every CTA
+// takes its part of both, and half of them take the private part first (64 sequences x 16384
+// shared and 100 to 1000 private tokens: 152 us, with one split 197).  Without pairs all items
+// are alike, and one split saves a run a CTA (16 sequences x 32768: 41 us, with two 45).
 struct Meta {
   int* gs;     // [ng + 1] first sequence of a group
   int* eff;    // [ng + 1] tokens of a group read once (a multiple of 128)
@@ -54,9 +60,19 @@ struct Meta {
   int* grp;    // [B] group of a sequence
   int* stepP;  // [B + 1] attention steps of private ranges before a sequence
   int* scP;    // [B + 1] score items of private ranges before a sequence
+  int* two;    // [1] whether the private items are split by themselves
 };
 
-__host__ __device__ inline int meta_ints(int B, int ng) { return 5 * (ng + 1) + 2 * B + 2 * (B + 1); }
+// What the combine kernel needs of a sequence, in one load; the record after the last sequence's
+// has the totals.
+struct __align__(16) SeqRec {
+  int n, eff;         // checked length; tokens read once for its group
+  int row0, pairs;    // its first query row among the group's; row-tile pairs of the group
+  int stepS, itemS;   // shared steps and items before its group
+  int stepP, two;     // private steps before it; Meta::two
+};
+
+__host__ __device__ inline int meta_ints(int B, int ng) { return 5 * (ng + 1) + 2 * B + 2 * (B + 1) + 1; }
 
 __device__ __forceinline__ Meta meta_at(int* base, int B, int ng) {
   Meta m;
@@ -69,6 +85,7 @@ __device__ __forceinline__ Meta meta_at(int* base, int B, int ng) {
   m.grp = m.nlen + B;
   m.stepP = m.grp + B;
   m.scP = m.stepP + B + 1;
+  m.two = m.scP + B + 1;
   return m;
 }
 
@@ -79,33 +96,35 @@ __device__ __forceinline__ void row_tiles(int members, const SharedParams& p, in
   odd = rt & 1;
 }
 
-constexpr int kPrepThreads = 1024;  // a thread a sequence, and a group (at most 1024 of each)
-
-// Exclusive scan over the CTA's threads; *total gets the sum.  All threads.
-__device__ int prep_scan(int v, int* sh, int* total) {
+// Exclusive scans of N values over a CTA of WARPS warps, and their totals.  All threads; sh is
+// not used again before the next barrier.
+template <int N, int WARPS>
+__device__ __forceinline__ void cta_scan(const int (&v)[N], int (&before)[N], int (&total)[N], int (*sh)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  int x[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += t;
+  for (int k = 0; k < N; ++k) {
+    x[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += t;
+    }
+    if (lane == 31) sh[k][warp] = x[k];
   }
-  if (lane == 31) sh[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int y = sh[lane];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {  // (every warp scans the warps' totals for itself)
+    const int mine = lane < WARPS ? sh[k][lane] : 0;
+    int y = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) y += t;
     }
-    sh[lane] = y;
+    total[k] = __shfl_sync(0xffffffffu, y, 31);
+    before[k] = __shfl_sync(0xffffffffu, y - mine, warp) + x[k] - v[k];
   }
-  __syncthreads();
-  const int r = (warp > 0 ? sh[warp - 1] : 0) + x - v;
-  *total = sh[31];
-  __syncthreads();
-  return r;
 }
 
 // Last index i in [0, n) with cum[i] <= x, skipping empty entries (cum[i] == cum[i + 1]).
@@ -118,17 +137,142 @@ __device__ __forceinline__ int find(const int* cum, int n, int x) {
   return lo;
 }
 
-// One CTA: the layout.  The other CTAs (with scores), one a sequence: the sum of its masked
-// query rows of each KV head, in fp32, as three bf16 parts whose sum is it to 2^-24.
-__global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const SharedParams p) {
-  __shared__ int gs[kMaxBatch + 1], least[kMaxBatch], eff_of[kMaxBatch], nlen[kMaxBatch], sh[32];
+// The layout, by a CTA of WARPS warps (all threads).  A length out of range makes its sequence's
+// nlen -1, groups that do not partition the batch or a shared length beyond a member's prefix
+// make the sequences' ranges private; the caller reports what is returned as false.
+template <int WARPS>
+__device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]) {
+  constexpr int NT = WARPS * 32, PER = (kMaxBatch + NT - 1) / NT;
+  const int tid = threadIdx.x, B = p.B, ng = p.n_groups, Hp = (p.Hkv + 1) / 2;
+  bool good = true;
+  for (int b = tid; b < B; b += NT) {
+    int n = p.prefix_len[b];
+    bool ok = n >= 0 && n <= p.max_len;
+    if (ok) {
+      if (p.ptab) {
+        ok = static_cast<int64_t>(n) + p.R <= static_cast<int64_t>(p.pstride) * p.psize;
+      } else {
+        const int64_t off = p.seq_offset[b];
+        ok = off >= 0 && off + static_cast<int64_t>(n) + p.R <= p.capacity;
+      }
+    }
+    good &= ok;
+    m.nlen[b] = ok ? n : -1;
+    m.grp[b] = 0;
+  }
+  int* least = m.stepS;   // (until the scan) the shortest member
+  int* shared = m.itemS;  // (until the scan) the shared length asked for
+  for (int g = tid; g <= ng; g += NT) {
+    m.gs[g] = p.group_start ? p.group_start[g] : (g ? B : 0);
+    if (g < ng) {
+      shared[g] = p.shared_len[g];
+      least[g] = 0x7fffffff;
+    }
+  }
+  __syncthreads();
+  bool shape = true;
+  for (int g = tid; g < ng; g += NT) shape &= m.gs[g] >= 0 && m.gs[g] <= m.gs[g + 1] && m.gs[g + 1] <= B;
+  if (tid == 0) shape &= m.gs[0] == 0 && m.gs[ng] == B;
+  shape = __syncthreads_and(shape);
+  good &= shape;
+  if (shape) {
+    for (int b = tid; b < B; b += NT) {
+      const int g = find(m.gs, ng, b);
+      m.grp[b] = g;
+      if (m.nlen[b] >= 0) atomicMin(&least[g], m.nlen[b]);
+    }
+  }
+  __syncthreads();
+  int steps[PER], items[PER], sc[PER], eff[PER], sum[3] = {0, 0, 0};
+  bool pair = false;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    steps[k] = items[k] = sc[k] = eff[k] = 0;
+    if (g < ng && shape && m.gs[g] < m.gs[g + 1]) {
+      const int members = m.gs[g + 1] - m.gs[g];
+      int most = least[g];
+      if (m.nlen[m.gs[g]] < 0) {
+        most = 0;  // no row to read the prefix through
+      } else if (shared[g] < 0 || shared[g] > most) {
+        good = false;
+        most = 0;
+      }
+      eff[k] = min(shared[g], most) / KT * KT;
+      int pairs, odd;
+      row_tiles(members, p, pairs, odd);
+      const int tiles = eff[k] / KT;
+      items[k] = tiles ? p.Hkv * pairs + odd * Hp : 0;
+      steps[k] = items[k] * (tiles + 1);
+      sc[k] = tiles * ((members + p.nsc - 1) / p.nsc);
+      pair |= tiles > 0 && pairs > 0;
+    }
+    sum[0] += steps[k];
+    sum[1] += items[k];
+    sum[2] += sc[k];
+  }
+  int at[3], tot[3];
+  pair = __syncthreads_or(pair);
+  cta_scan<3, WARPS>(sum, at, tot, sh);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    if (g < ng) {
+      m.eff[g] = eff[k];
+      m.stepS[g] = at[0];
+      m.itemS[g] = at[1];
+      m.scS[g] = at[2];
+    }
+    at[0] += steps[k];
+    at[1] += items[k];
+    at[2] += sc[k];
+  }
+  if (tid == 0) {
+    m.eff[ng] = 0;
+    m.stepS[ng] = tot[0];
+    m.itemS[ng] = tot[1];
+    m.scS[ng] = tot[2];
+    *m.two = pair;
+  }
+  __syncthreads();
+  int tiles[PER], sum2[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int b = tid * PER + k;
+    tiles[k] = b < B && m.nlen[b] >= 0 ? (m.nlen[b] - m.eff[m.grp[b]] + KT - 1) / KT : 0;
+    sum2[0] += tiles[k] > 0 ? (tiles[k] + 1) * Hp : 0;
+    sum2[1] += tiles[k];
+  }
+  int at2[2], tot2[2];
+  cta_scan<2, WARPS>(sum2, at2, tot2, sh);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int b = tid * PER + k;
+    if (b < B) {
+      m.stepP[b] = at2[0];
+      m.scP[b] = at2[1];
+    }
+    at2[0] += tiles[k] > 0 ? (tiles[k] + 1) * Hp : 0;
+    at2[1] += tiles[k];
+  }
+  if (tid == 0) {
+    m.stepP[B] = tot2[0];
+    m.scP[B] = tot2[1];
+  }
+  __syncthreads();
+  return good;
+}
+
+// The first kernel of a call.  CTA 0: the layout.  The others (with scores), one a sequence: the sum
+// of its masked query rows of each KV head, in fp32, as three bf16 parts whose sum is it to 2^-24.
+__global__ void __launch_bounds__(1024) shared_prep_kernel(const SharedParams p) {
+  __shared__ int space[5 * (kMaxBatch + 1) + 2 * kMaxBatch + 2 * (kMaxBatch + 1) + 1], sh[3][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
     const int b = blockIdx.x - 1, width = p.Hkv * p.D;
     const size_t part = static_cast<size_t>(p.Bpad) * width;
-    for (int e = tid; e < width; e += kPrepThreads) {
+    for (int e = threadIdx.x; e < width; e += 1024) {
       const int g = e / p.D, d = e - g * p.D;
       float acc = 0.f;
       for (uint32_t bits = p.mask; bits != 0u; bits &= bits - 1u) {
@@ -147,92 +291,20 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const SharedP
     }
     return;
   }
-  const int B = p.B, ng = p.n_groups, Hp = (p.Hkv + 1) / 2;
-  const Meta m = meta_at(p.meta, B, ng);
-  bool bad = false;
-  int n = -1, shared = 0;
-  if (tid < B) {
-    n = p.prefix_len[tid];
-    bool ok = n >= 0 && n <= p.max_len;
-    if (ok) {
-      if (p.ptab) {
-        ok = static_cast<int64_t>(n) + p.R <= static_cast<int64_t>(p.pstride) * p.psize;
-      } else {
-        const int64_t off = p.seq_offset[tid];
-        ok = off >= 0 && off + static_cast<int64_t>(n) + p.R <= p.capacity;
-      }
+  const Meta m = meta_at(space, p.B, p.n_groups);
+  if (!build_layout<32>(p, m, sh)) report(p.status, VG_ERR_DEVICE_BOUNDS);
+  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += 1024) p.meta[i] = space[i];
+  SeqRec* rec = reinterpret_cast<SeqRec*>(p.rec);
+  for (int b = threadIdx.x; b <= p.B; b += 1024) {
+    if (b == p.B) {
+      rec[b] = SeqRec{0, 0, 0, 0, m.stepS[p.n_groups], m.itemS[p.n_groups], m.stepP[p.B], *m.two};
+    } else {
+      const int g = m.grp[b];
+      int pairs, odd;
+      row_tiles(m.gs[g + 1] - m.gs[g], p, pairs, odd);
+      rec[b] = SeqRec{m.nlen[b], m.eff[g], (b - m.gs[g]) * p.M, pairs, m.stepS[g], m.itemS[g], m.stepP[b], 0};
     }
-    bad = !ok;
-    if (!ok) n = -1;
-    nlen[tid] = n;
   }
-  if (tid < ng) {
-    gs[tid] = p.group_start ? p.group_start[tid] : 0;
-    shared = p.shared_len[tid];
-    least[tid] = 0x7fffffff;
-  }
-  if (tid == 0) gs[ng] = p.group_start ? p.group_start[ng] : B;
-  __syncthreads();
-  bool shape = true;
-  if (tid < ng) shape = gs[tid] >= 0 && gs[tid] <= gs[tid + 1] && gs[tid + 1] <= B;
-  if (tid == 0) shape = shape && gs[0] == 0 && gs[ng] == B;
-  shape = __syncthreads_and(shape);
-  int grp = 0;
-  if (tid < B && shape) {
-    grp = find(gs, ng, tid);
-    if (n >= 0) atomicMin(&least[grp], n);
-  }
-  __syncthreads();
-  int steps = 0, items = 0, sc = 0, eff = 0;
-  if (tid < ng && shape && gs[tid] < gs[tid + 1]) {
-    const int members = gs[tid + 1] - gs[tid];
-    int most = least[tid];
-    if (nlen[gs[tid]] < 0) {
-      most = 0;  // no row to read the prefix through (that row's length is reported)
-    } else if (shared < 0 || shared > most) {
-      bad = true;
-      most = 0;
-    }
-    eff = min(shared, most) / KT * KT;
-    int pairs, odd;
-    row_tiles(members, p, pairs, odd);
-    const int tiles = eff / KT;
-    items = tiles ? p.Hkv * pairs + odd * Hp : 0;
-    steps = items * (tiles + 1);
-    sc = tiles * ((members + p.nsc - 1) / p.nsc);
-  }
-  if (tid < ng) eff_of[tid] = eff;
-  int totS, totI, totC, totP;
-  const int s0 = prep_scan(steps, sh, &totS), i0 = prep_scan(items, sh, &totI), c0 = prep_scan(sc, sh, &totC);
-  if (tid < ng) {
-    m.gs[tid] = gs[tid];
-    m.eff[tid] = eff;
-    m.stepS[tid] = s0;
-    m.itemS[tid] = i0;
-    m.scS[tid] = c0;
-  }
-  // (eff_of is complete: the scans synchronised)
-  const int tiles = tid < B && n >= 0 ? (n - eff_of[grp] + KT - 1) / KT : 0;
-  const int cost = tiles > 0 ? tiles + 1 : 0;
-  const int p0 = prep_scan(cost, sh, &totP);
-  int totT;
-  const int t0 = prep_scan(tiles, sh, &totT);
-  if (tid < B) {
-    m.nlen[tid] = n;
-    m.grp[tid] = grp;
-    m.stepP[tid] = p0 * Hp;
-    m.scP[tid] = t0;
-  }
-  if (tid == 0) {
-    m.gs[ng] = B;
-    m.eff[ng] = 0;
-    m.stepS[ng] = totS;
-    m.itemS[ng] = totI;
-    m.scS[ng] = totC;
-    m.stepP[B] = totP * Hp;
-    m.scP[B] = totT;
-  }
-  if (bad || (!shape && tid == 0)) report(p.status, VG_ERR_DEVICE_BOUNDS);
 }
 
 // A contiguous run of key tiles of one item, as one CTA works on it.
@@ -249,13 +321,41 @@ struct Run {
   int item;           // index of its partials among the shared / private items
 };
 
-// The run at step x of a CTA that ends at xend; x moves past it (ntiles may be 0).
-__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int& x, int xend) {
+// The split of the shared (part 0) or private steps: T steps over nc CTAs, as many as have one;
+// the part's step x is step x + first of them.
+struct Split {
+  int T, nc, first;
+};
+__device__ __forceinline__ Split split_of(int part, int totS, int totP, bool two, int nctas) {
+  const int T = two ? (part ? totP : totS) : totS + totP;
+  return Split{T, min(T, nctas), part && !two ? totS : 0};
+}
+
+// The steps of a part that this CTA owns, from the value returned up to x1; cta: its index in the
+// part's split.  (A private split of its own runs from the other end of the grid, so that the few
+// steps of a small one fall to other CTAs than the first shared ones.)
+__device__ __forceinline__ int my_steps(const SharedParams& p, const Meta& m, int part, int& x1, int& cta) {
+  const int totS = m.stepS[p.n_groups], totP = m.stepP[p.B];
+  const bool two = *m.two != 0;
+  const Split s = split_of(part, totS, totP, two, p.nctas);
+  const int tot = part ? totP : totS;
+  cta = part && two ? p.nctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+  x1 = 0;
+  if (cta >= s.nc) return 0;
+  x1 = min(static_cast<int>(split_begin(cta + 1, s.T, s.nc)) - s.first, tot);
+  return min(max(static_cast<int>(split_begin(cta, s.T, s.nc)) - s.first, 0), tot);
+}
+// A CTA's parts in the order it works on them.
+__device__ __forceinline__ int part_of(const Meta& m, int pass) {
+  return pass ^ (*m.two ? static_cast<int>(blockIdx.x & 1) : 0);
+}
+
+// The run at step x of a part, of a CTA that ends at xend; x moves past it (ntiles may be 0).
+__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int part, int& x, int xend) {
   Run r;
   const int Hp = (p.Hkv + 1) / 2;
-  const int totS = m.stepS[p.n_groups];
   int off, len;  // step within the item, the item's steps
-  if (x < totS) {
+  if (part == 0) {
     const int g = find(m.stepS, p.n_groups, x);
     const int members = m.gs[g + 1] - m.gs[g];
     int pairs, odd;
@@ -284,11 +384,10 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
       r.r0[0] = r.r0[1] = pairs * 2 * p.RT;
     }
   } else {
-    const int y = x - totS;
-    const int b = find(m.stepP, p.B, y);
+    const int b = find(m.stepP, p.B, x);
     const int eff = m.eff[m.grp[b]];
     len = (m.nlen[b] - eff + KT - 1) / KT + 1;
-    off = y - m.stepP[b];
+    off = x - m.stepP[b];
     const int hp = off / len;
     off -= hp * len;
     r.row = r.seq0 = b;
@@ -339,7 +438,22 @@ struct SCfg {
   }
 };
 
-// 64 columns of this thread's tensor-memory lane, loaded and waited for in one statement.
+// Three times 16 columns of this thread's tensor-memory lane, loaded and waited for in one
+// statement.
+__device__ __forceinline__ void tc_ld16x3_sync(uint32_t t0, uint32_t t1, uint32_t t2, float (&v)[3][16]) {
+  uint32_t r[48];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%49];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%50];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]), "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]), "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47])
+      : "r"(t0), "r"(t1), "r"(t2)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 48; ++i) v[i / 16][i % 16] = __uint_as_float(r[i]);
+}
+// 64 columns, likewise.
 __device__ __forceinline__ void tc_ld64_sync(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
   asm volatile(
@@ -370,7 +484,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
   return ok != 0;
 }
-// tma_load_2d to a shared-memory address.
+// tma_load_2d to a shared-memory address; 3-D.
 __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
                                                uint64_t* bar) {
   asm volatile(
@@ -379,7 +493,6 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// 3-D tiled TMA load, as tma_load_2d_at.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                             uint64_t* bar) {
   asm volatile(
@@ -439,31 +552,34 @@ __device__ __forceinline__ void tc_commit_one(uint32_t lead, uint64_t* bar) {
       : "memory");
 }
 
-// mbar_wait_ab for a whole warp, its tries suspended for up to 20 us each: a waiting warp that
-// polls takes issue slots from the softmax warps of its SM partition.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort) {
-  bool ok = false;
-  const uint32_t addr = smem_u32(bar);
-  unsigned long long t0 = 0;
+// One try of a phase for a whole warp, suspended for up to 20 us.
+__device__ __forceinline__ bool warp_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
+}
+// The rest of a wait that the first try did not end (not inlined: a kernel of several roles is
+// slow to start while its code is not in the instruction cache).
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, int32_t* status, volatile int* abort) {
+  const unsigned long long t0 = globaltimer();
   while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity), "r"(20000u)
-        : "memory");
-    if (__all_sync(0xffffffffu, done != 0)) return true;
-    if (*abort) break;
-    const unsigned long long t = globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) {
+    if (warp_try(bar, parity)) return true;
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
       *abort = 1;
       report(status, VG_ERR_DEVICE_TIMEOUT);
-      break;
+      return false;
     }
   }
-  __syncwarp();
-  return ok;
+}
+// mbar_wait_ab for a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  return warp_try(addr, parity) || warp_wait_on(addr, parity, status, abort);
 }
 
 // Wait until use number (lap, slot) of a ring is filled.  A wait by parity is right only while
@@ -533,19 +649,20 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 17) tc_alloc(tmem_slot, C::TMEM_COLS);
-  pdl_wait();
-  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += C::THREADS) mbase[i] = p.meta[i];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tmem_slot;
-  pdl_launch_dependents();
+  // Nothing in global memory is read before this; every thread calls it once.
+  auto begin = [&] {
+    pdl_wait();
+    for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += C::THREADS) mbase[i] = p.meta[i];
+    __syncthreads();
+    pdl_launch_dependents();
+  };
 
-  const int T = m.stepS[p.n_groups] + m.stepP[p.B];
-  const int x0 = static_cast<int>(split_begin(blockIdx.x, T, p.nctas));
-  const int x1 = static_cast<int>(split_begin(blockIdx.x + 1, T, p.nctas));
-
-  if (x0 < x1 && (warp == 16 || warp == 18)) {
+  if (warp == 16 || warp == 18) {
+    begin();
     // ---------------------------------------------------------------- TMA producers
     // A tile is 128 / box_rows boxes (page pieces) of 64 columns: one box a lane, the boxes of
     // every tile dealt out to two warps in turn (a warp issues its lanes' boxes one by one).
@@ -555,32 +672,26 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     }
     const int BR = p.box_rows;
     const int e = 2 * lane + (warp == 18 ? 1 : 0);
-    const int box = e / C::HALVES;
+    const int box = e / C::HALVES, half = e % C::HALVES;
     const bool has_box = box < KT / BR;
-    const uint32_t ring0 = smem_u32(ring);
+    const uint32_t dst0 = smem_u32(ring) + half * C::HALF_BYTES + box * BR * 128;
     int off0 = 0;
     int u = 0, st = 0, lap = 0;  // ring uses so far, slot and lap of the next one
     bool ok = true;
     const bool leader = elect_one();
-    // a warp's boxes: one a lane, issued by one thread (an issue takes uniform operands: lanes
-    // issuing their own boxes would be run one by one with more work for each)
-    const int nb = KT / BR * C::HALVES, mine = (nb + (warp == 16 ? 1 : 0)) / 2;
+    const int sh = (p.psize & (p.psize - 1)) == 0 ? __ffs(p.psize) - 1 : -1;  // (most page sizes)
+    bool zeros = false;  // a slot may hold zeros that the softmax warps wrote
     auto load = [&](const CUtensorMap* map, int head, int y) {
       if (lap > 0) ok = warp_wait(&empty[st], (lap - 1) & 1, p.status, abort);
       if (!ok) return;
       const uint32_t have = __ballot_sync(0xffffffffu, y >= 0);
       if (leader) {
-        fence_proxy_async_smem();  // the slot may hold zeros written by the generic proxy
+        if (zeros) fence_proxy_async_smem();
         mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(have) * BR * 128));
       }
-      for (int i = 0; i < mine; ++i) {
-        const int yi = __shfl_sync(0xffffffffu, y, i);
-        const int ei = 2 * i + (warp == 18 ? 1 : 0);
-        const int bi = ei / C::HALVES, hi = ei % C::HALVES;
-        if (leader && yi >= 0)
-          tma_load_2d_at(ring0 + st * C::TILE_BYTES + hi * C::HALF_BYTES + bi * BR * 128, map, head * D + hi * 64, yi,
-                         &full[st]);
-      }
+      __syncwarp();
+      if (y >= 0)
+        tma_load_2d_at(dst0 + st * C::TILE_BYTES, map, head * D + half * 64, y, &full[st]);
       __syncwarp();
       ++u;
       if (++st == NS) {
@@ -590,8 +701,10 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     };
     const int lw = warp == 18 ? 1 : 0;  // this warp brings the query tiles of that lane
     uint32_t qpar = 1;                  // (the first wait passes)
-    for (int x = x0; ok && x < x1;) {
-      const Run r = make_run(p, m, x, x1);
+    for (int pass = 0; pass < 2; ++pass) {
+     int x1, cta;
+     for (int x = my_steps(p, m, part_of(m, pass), x1, cta); ok && x < x1;) {
+      const Run r = make_run(p, m, part_of(m, pass), x, x1);
       if (r.ntiles == 0) continue;
       // page-table word of this lane's box in tile n, loaded a tile ahead; its slot row (-1: no
       // box, or reported) when the tile is issued
@@ -599,7 +712,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         const int tok = (r.tile0 + n) * KT + box * BR;
         if (!has_box || n >= r.ntiles || tok >= r.ntok) return -1;
         if (!p.ptab) return 0;
-        const int pi = (r.tok0 + tok) / p.psize;
+        const int pi = sh >= 0 ? (r.tok0 + tok) >> sh : (r.tok0 + tok) / p.psize;
         return pi < p.pstride ? p.ptab[static_cast<size_t>(r.row) * p.pstride + pi] : -1;
       };
       auto slot_row = [&](int n, int w) {
@@ -610,7 +723,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           report(p.status, VG_ERR_DEVICE_BOUNDS);
           return -1;
         }
-        return w * p.psize + (r.tok0 + tok) % p.psize;
+        return w * p.psize + (sh >= 0 ? (r.tok0 + tok) & (p.psize - 1) : (r.tok0 + tok) % p.psize);
       };
       off0 = p.ptab ? 0 : static_cast<int>(p.seq_offset[r.row]);
       int w0 = word(0), w1 = word(1);
@@ -642,6 +755,8 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         y = yn;
         w1 = w2;
       }
+      zeros |= r.priv;
+     }
     }
     // No copy may still be in flight when the CTA exits: normally the issuers have waited
     // for every one; after a lost wait the last ones issued here get 2 ms each to land.
@@ -651,7 +766,8 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         mbar_wait_ab(&full[i % NS], (i / NS) & 1, nullptr, &never, 2000000ull);
     }
     __syncwarp();
-  } else if (x0 < x1 && (warp == 17 || warp == 19)) {
+  } else if (warp == 17 || warp == 19) {
+    begin();
     // ---------------------------------------------------------------- MMA issuers, one a lane
     // The whole warp waits, one elected thread issues.  Descriptors are a base plus offsets in
     // units of 16 bytes (addresses stay below 2^18, so the sums stay in the address field).
@@ -705,8 +821,10 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       const int s2 = st + ahead < NS ? st + ahead : st + ahead - NS;
       return filled(full, empty, s2, st + ahead < NS ? lap : lap + 1, p.status, abort);
     };
-    for (int x = x0; ok && x < x1;) {
-      const Run r = make_run(p, m, x, x1);
+    for (int pass = 0; pass < 2; ++pass) {
+     int x1, cta;
+     for (int x = my_steps(p, m, part_of(m, pass), x1, cta); ok && x < x1;) {
+      const Run r = make_run(p, m, part_of(m, pass), x, x1);
       const int ntiles = __shfl_sync(0xffffffffu, r.ntiles, 0), mode = __shfl_sync(0xffffffffu, r.mode, 0);
       if (ntiles == 0) continue;
       const int last = ntiles - 1;
@@ -743,10 +861,11 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         }
         if (!w) skip(theirs);
       }
+     }
     }
     tc_commit_one(lead, &fin[w]);  // every MMA of this thread complete before the CTA tears down
     warp_wait(&fin[w], 0, p.status, abort);
-  } else if (x0 < x1 && warp < 16) {
+  } else {
     // ---------------------------------------------------------------- softmax lanes
     // Two threads a row: half 0 takes keys 0 .. 63 of each tile, half 1 the others, and each half
     // of the output's columns where those are touched.  They use one running maximum, the row's
@@ -760,8 +879,23 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     const uint32_t ts = tq + w * 128, to = tq + C::COL_O + w * D + half * (D / 2);
     const float c2 = p.scale_log2;
     int base = 0, ns = 0, nr = 0;  // ring uses, tiles and runs of this lane so far
-    for (int x = x0; x < x1;) {
-      const Run r = make_run(p, m, x, x1);
+    // Pass -1 runs a tile of whatever tensor memory holds through the code, without a wait, an
+    // arrival or a store, while the previous kernel ends and the first tiles are on their way:
+    // the first real tile then finds its instructions in the caches (it took 11,000 cycles to
+    // go from S to P without that, of a decode step's 75,000).
+    for (int pass = -1; pass < 2; ++pass) {
+     const bool real = pass >= 0;
+     int x = 0, x1 = 1, cta = 0;
+     if (pass == 0) begin();
+     if (real) x = my_steps(p, m, part_of(m, pass), x1, cta);
+     while (x < x1) {
+      Run r;
+      if (real) {
+        r = make_run(p, m, part_of(m, pass), x, x1);
+      } else {
+        r = Run{kPair, 0, 1, 0, 0, KT, 0, 2 * KT, {0, 0}, {0, 0}, false, 0};
+        x = x1;
+      }
       if (r.ntiles == 0) continue;
       if (r.mode == kSingle && w == 1) {
         base += run_uses(r.mode, r.ntiles);
@@ -773,8 +907,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       float mx = neg_inf(), l = 0.f;        // the maximum in use (log2 units), this half's sum
       for (int n = 0; n < r.ntiles; ++n) {
         const int left = r.ntok - (r.tile0 + n) * KT;  // keys of the tile (128 or more: all)
-        warp_wait(&s_full[w], ns & 1, p.status, abort);
-        ++ns;
+        if (real) warp_wait(&s_full[w], ns++ & 1, p.status, abort);
         tc_fence_after();
         if (left < KT) {
           // value rows past the range hold whatever was there: zeroed, so that 0 * V is 0 (after
@@ -850,12 +983,15 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           mx = mn;
         }
         l += ls;
-        tc_st32b(ts + (HK / 2) * half, pk);
-        tc_wait_st();
+        if (real) {
+          tc_st32b(ts + (HK / 2) * half, pk);
+          tc_wait_st();
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        if (real && lane == 0) mbar_arrive(&p_full[w]);
       }
+      if (!real) break;
       // the run's partial: (O, max, sum) of each row once P V of its last tile has landed
       warp_wait(&o_full[w], nr & 1, p.status, abort);
       ++nr;
@@ -863,7 +999,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       if (live) {
         // four columns of 32 rows lie together: a warp's stores are 512 contiguous bytes
         const int height = r.priv ? p.Mpad : KT;
-        const size_t unit = static_cast<size_t>(blockIdx.x + r.item) * 2 + w;
+        const size_t unit = static_cast<size_t>(cta + r.item) * 2 + w;
         float* po = (r.priv ? p.partp_o : p.parts_o) + (unit * D + half * (D / 2)) * height + row * 4;
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -885,6 +1021,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       }
       tc_fence_before();
       base += run_uses(r.mode, r.ntiles);
+     }
     }
   }
   __syncwarp();
@@ -897,183 +1034,253 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------- combine
-// A CTA merges eight consecutive rows of a (sequence, KV head).  First a warp a row: the
-// causal logits of the row's own keys u = 0 .. t, the maximum and the sum over those and the
-// row's partials (lanes across partials).  Then a thread a (row, four columns): the partials
-// of the row's shared item by CTA, of its private item by CTA, then the causal values: a fixed
-// order.
-constexpr int kCombRows = 8;
-
-template <int D>
+// A CTA merges ROWS consecutive rows of a (sequence, KV head).  A thread has four columns of every
+// eighth row (ROWS >= 8), or of one row and every fourth of its partials (ROWS = 2).  Everything
+// is asked for in two rounds: the sequence's record, then the partials, their maxima and sums, the
+// query rows and the verify rows' own keys and values; where each of these lies is worked out
+// once, by one thread each.  A warp a row takes the causal logits of the row's own keys
+// u = 0 .. t, and the maximum and the sum over those and the row's partials (lanes across
+// partials).  Then the threads of a column add up: the row's shared partials by CTA, its
+// private ones by CTA, the causal values: a fixed order.
+//
+// What bounds it is instructions, most of them addresses and the short sums (64 sequences x 32 rows
+// x 8 heads: 30 us at 0.7 instructions a cycle and partition; 16 or 32 rows a CTA are no faster).
+template <int D, int ROWS>
 __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParams p) {
-  constexpr int PER = D / 32, WARPS = D / 16, CH = D / 8;
-  __shared__ float lgs[kCombRows][16], rowM[kCombRows], rowL[kCombRows];
-  __shared__ int seg[kCombRows][4];        // first CTA and count of the row's shared, private partials
-  __shared__ size_t at[kCombRows][2];      // unit row of the first of each
+  constexpr int PER = D / 32, WARPS = D / 16, CH = D / 8, NT = 2 * D;
+  constexpr int SG = ROWS < 8 ? 8 / ROWS : 1;      // threads that share a row's four columns
+  constexpr int RPT = ROWS < 8 ? 1 : ROWS / 8;     // rows a thread
+  constexpr int NB = ROWS == 2 ? 8 : 4;            // partials in flight a thread
+  __shared__ float lgs[ROWS][16], rowM[ROWS], rowL[ROWS];
+  // the row's shared and private partials: how many, and the first one's place in units of 16
+  // bytes (of O, then of its row of maximum and sums)
+  __shared__ int cnt[ROWS][2];
+  __shared__ uint32_t at[ROWS][4];
+  __shared__ int64_t slots[16];  // of the verify rows in the cache
   __shared__ __align__(16) __nv_bfloat16 kvs[2][16][D];
+  __shared__ float4 part_sum[SG][ROWS][D / 4];
   pdl_launch_dependents();
-  pdl_wait();
-  const Meta m = meta_at(p.meta, p.B, p.n_groups);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rblocks = (p.M + kCombRows - 1) / kCombRows;
-  const int bg = blockIdx.x / rblocks, r0 = (blockIdx.x - bg * rblocks) * kCombRows;
-  const int g = bg % p.Hkv, b = bg / p.Hkv;
-  const int n = m.nlen[b], grp = m.grp[b], eff = m.eff[grp], gs0 = m.gs[grp], gs1 = m.gs[grp + 1];
-  const int stepS = m.stepS[grp], itemS = m.itemS[grp], totS = m.stepS[p.n_groups], stepP = m.stepP[b];
-  const int T = totS + m.stepP[p.B];
-  if (n < 0) return;  // the whole CTA
-  const int rows = min(kCombRows, p.M - r0);
+  const int rblocks = (p.M + ROWS - 1) / ROWS;
+  const int bg = blockIdx.x / rblocks, r0 = (blockIdx.x - bg * rblocks) * ROWS;
+  const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+  const int rows = min(ROWS, p.M - r0);
   const int tmax = (r0 + rows - 1) / p.G;
-  for (int e = tid; e < 2 * (tmax + 1) * CH; e += 2 * D) {
-    const int which = e / ((tmax + 1) * CH), rem = e - which * (tmax + 1) * CH;
-    const int u = rem / CH, c = rem - u * CH;
-    const __nv_bfloat16* fresh = which ? p.v_new : p.k_new;
-    const __nv_bfloat16* src = nullptr;
-    if (fresh) {
-      src = fresh + ((static_cast<size_t>(b) * p.R + u) * p.Hkv + g) * D;
-    } else {
-      const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + u);
-      if (slot >= 0) src = (which ? p.V : p.K) + (slot * p.Hkv + g) * D;
-    }
-    reinterpret_cast<uint4*>(&kvs[which][u][0])[c] =
-        src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-  }
-  __syncthreads();
-  for (int rl = warp; rl < rows; rl += WARPS) {
-    const int r = r0 + rl, t = r / p.G, jh = r - t * p.G;
-    // where the row's partials are: an item's tiles are its steps but the first, and a CTA that
-    // owns one of those left a partial
-    int cs = 0, nS = 0, cp = 0, nP = 0;
-    size_t baseS = 0, baseP = 0;
-    const int tiles = eff / KT, ptiles = (n - eff + KT - 1) / KT;
+  pdl_wait();
+  const SeqRec rec = reinterpret_cast<const SeqRec*>(p.rec)[b];
+  const int n = rec.n;
+  if (n < 0) return;  // the whole CTA
+  if (tid < rows) {
+    // an item's tiles are its steps but the first, and every CTA that owns one of those left a
+    // partial
+    const SeqRec tot = reinterpret_cast<const SeqRec*>(p.rec)[p.B];
+    const int r = r0 + tid, tiles = rec.eff / KT, ptiles = (n - rec.eff + KT - 1) / KT;
+    cnt[tid][0] = cnt[tid][1] = 0;
     if (tiles > 0) {
-      int pairs, odd;
-      row_tiles(gs1 - gs0, p, pairs, odd);
-      const int rr = (b - gs0) * p.M + r, rt = rr / p.RT;
-      const bool pair = (rt >> 1) < pairs;
-      const int it = pair ? g * pairs + (rt >> 1) : p.Hkv * pairs + (g >> 1), w = pair ? rt & 1 : g & 1;
-      const int s0 = stepS + it * (tiles + 1);
-      cs = static_cast<int>(owner_cta(s0 + 1, T, p.nctas));
-      nS = static_cast<int>(owner_cta(s0 + tiles, T, p.nctas)) - cs + 1;
-      baseS = (static_cast<size_t>(cs + itemS + it) * 2 + w) * KT * D + static_cast<size_t>(rr - rt * p.RT);
+      const Split sp = split_of(0, tot.stepS, tot.stepP, tot.two, p.nctas);
+      const int rr = rec.row0 + r, rt = rr / p.RT;
+      const bool pair = (rt >> 1) < rec.pairs;
+      const int it = pair ? g * rec.pairs + (rt >> 1) : p.Hkv * rec.pairs + (g >> 1);
+      const int s0 = rec.stepS + it * (tiles + 1) + sp.first;
+      const int cs = static_cast<int>(owner_cta(s0 + 1, sp.T, sp.nc));
+      cnt[tid][0] = static_cast<int>(owner_cta(s0 + tiles, sp.T, sp.nc)) - cs + 1;
+      const uint32_t u = (cs + rec.itemS + it) * 2 + (pair ? rt & 1 : g & 1);
+      at[tid][0] = u * (KT * D / 4) + (rr - rt * p.RT);
+      at[tid][1] = u * KT + (rr - rt * p.RT);
     }
     if (ptiles > 0) {
-      const int Hp = (p.Hkv + 1) / 2;
-      const int s0 = totS + stepP + (g >> 1) * (ptiles + 1);
-      cp = static_cast<int>(owner_cta(s0 + 1, T, p.nctas));
-      nP = static_cast<int>(owner_cta(s0 + ptiles, T, p.nctas)) - cp + 1;
-      baseP = (static_cast<size_t>(cp + b * Hp + (g >> 1)) * 2 + (g & 1)) * p.Mpad * D + r;
+      const Split sp = split_of(1, tot.stepS, tot.stepP, tot.two, p.nctas);
+      const int s0 = rec.stepP + (g >> 1) * (ptiles + 1) + sp.first;
+      const int cp = static_cast<int>(owner_cta(s0 + 1, sp.T, sp.nc));
+      cnt[tid][1] = static_cast<int>(owner_cta(s0 + ptiles, sp.T, sp.nc)) - cp + 1;
+      const uint32_t u = (cp + b * ((p.Hkv + 1) / 2) + (g >> 1)) * 2 + (g & 1);
+      at[tid][2] = u * (p.Mpad * (D / 4)) + r;
+      at[tid][3] = u * p.Mpad + r;
     }
-    // (max, sum) of partial i; a CTA without steps wrote none
-    auto load_ml = [&](int i, float& ms, float& ls) {
-      ms = neg_inf();
-      ls = 0.f;
-      if (i >= nS + nP || !split_nonempty(i < nS ? cs + i : cp + i - nS, T, p.nctas)) return;
-      const float* src =
-          i < nS ? p.parts_ml + ((baseS / (KT * D) + 2 * static_cast<size_t>(i)) * KT + baseS % (KT * D)) * 4
-                 : p.partp_ml + ((baseP / (static_cast<size_t>(p.Mpad) * D) + 2 * static_cast<size_t>(i - nS)) * p.Mpad + r) * 4;
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      ms = v.x;
-      ls = v.y + v.z;
-    };
-    float pm, pl;
-    load_ml(lane, pm, pl);
+  } else if (tid >= 32 && tid < 48 && tid - 32 <= tmax) {
+    slots[tid - 32] = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + tid - 32);
+  }
+  __syncthreads();
+  // (max, sum) row and O of partial i of a row (from one CTA's partial to the next's two lanes' rows
+  // lie between)
+  auto ml_at = [&](int rl, int i, int nS) {
+    return i < nS ? reinterpret_cast<const float4*>(p.parts_ml) + (at[rl][1] + static_cast<uint32_t>(i) * (2 * KT))
+                  : reinterpret_cast<const float4*>(p.partp_ml) + (at[rl][3] + static_cast<uint32_t>(i - nS) * (2 * p.Mpad));
+  };
+  auto o_at = [&](int rl, int i, int nS, int c) {
+    return i < nS ? reinterpret_cast<const float4*>(p.parts_o) +
+                        (at[rl][0] + static_cast<uint32_t>(i) * (2 * KT * D / 4) + c * KT)
+                  : reinterpret_cast<const float4*>(p.partp_o) +
+                        (at[rl][2] + static_cast<uint32_t>(i - nS) * (2 * p.Mpad * (D / 4)) + c * p.Mpad);
+  };
+  const int rl0 = tid % (ROWS < 8 ? ROWS : 8), sg = ROWS < 8 ? tid / ROWS % SG : 0, c = tid / 8;
+  struct Batch {
+    float ml[NB];
+    float4 v[NB];
+  };
+  auto fetch = [&](Batch& x, int rl, int i0) {  // partials i0 + sg, i0 + sg + SG ... of a row
+    const int nS = rl < rows ? cnt[rl][0] : 0, nseg = rl < rows ? nS + cnt[rl][1] : 0;
+#pragma unroll
+    for (int q = 0; q < NB; ++q) {
+      const int i = i0 + sg + q * SG;
+      x.ml[q] = neg_inf();
+      x.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < nseg) {
+        x.ml[q] = ml_at(rl, i, nS)->x;
+        x.v[q] = *o_at(rl, i, nS, c);
+      }
+    }
+  };
+  Batch now, next;
+  fetch(now, rl0, 0);
+  for (int e = tid; e < 2 * 16 * CH; e += NT) {
+    const int which = e / (16 * CH), u = e / CH % 16, cc = e % CH;
+    if (u > tmax) continue;
+    const __nv_bfloat16* fresh = which ? p.v_new : p.k_new;
+    const int64_t slot = slots[u];
+    const __nv_bfloat16* src = fresh ? fresh + ((static_cast<size_t>(b) * p.R + u) * p.Hkv + g) * D
+                                     : (which ? p.V : p.K) + ((slot < 0 ? 0 : slot) * p.Hkv + g) * D;
+    uint4 x = reinterpret_cast<const uint4*>(src)[cc];
+    if (!fresh && slot < 0) x = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4*>(&kvs[which][u][0])[cc] = x;
+  }
+  __syncthreads();
+  auto load_ml = [&](int rl, int i, float& ms, float& ls) {  // (max, sum) of partial i of a row
+    ms = neg_inf();
+    ls = 0.f;
+    if (rl >= rows) return;
+    const int nS = cnt[rl][0];
+    if (i >= nS + cnt[rl][1]) return;
+    const float4 x = *ml_at(rl, i, nS);
+    ms = x.x;
+    ls = x.y + x.z;
+  };
+  // the first maxima and sums and the query row of each of the warp's rows, asked for together
+  constexpr int RPW = (ROWS + WARPS - 1) / WARPS;
+  float first_m[RPW][2], first_l[RPW][2];
+  uint32_t qrow[RPW][PER / 2];
+#pragma unroll
+  for (int k = 0; k < RPW; ++k) {
+    const int wr = warp + k * WARPS;
+    load_ml(wr, lane, first_m[k][0], first_l[k][0]);
+    load_ml(wr, lane + 32, first_m[k][1], first_l[k][1]);
+    const int r = r0 + min(wr, rows - 1), t = r / p.G, jh = r - t * p.G;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        p.q + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) qrow[k][e] = src[e];
+  }
+#pragma unroll
+  for (int kr = 0; kr < RPW; ++kr) {
+    const int wr = warp + kr * WARPS;
+    if (wr >= rows) break;
+    const int t = (r0 + wr) / p.G;
+    const int np = cnt[wr][0] + cnt[wr][1];
+    const float pm = first_m[kr][0], pl = first_l[kr][0], pm2 = first_m[kr][1], pl2 = first_l[kr][1];
     float qv[PER];
-    const __nv_bfloat16* qrow = p.q + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + lane * PER;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) qv[e] = __bfloat162float(qrow[e]);
-    float M = neg_inf();
-    for (int u = 0; u <= t; ++u) {
-      float acc = 0.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc += qv[e] * __bfloat162float(kvs[0][u][lane * PER + e]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      acc *= p.scale_log2;
-      M = fmaxf(M, acc);
-      if (lane == 0) lgs[rl][u] = acc;
+    for (int e = 0; e < PER / 2; ++e) {
+      qv[2 * e] = __uint_as_float(qrow[kr][e] << 16);
+      qv[2 * e + 1] = __uint_as_float(qrow[kr][e] & 0xffff0000u);
     }
-    float pmax = pm;
-    for (int i = 32; i < nS + nP; i += 32) {
+    float M = neg_inf();
+    for (int u0 = 0; u0 <= t; u0 += 4) {  // (four keys at a time: their sums overlap)
+      float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (u0 + j <= t) {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) dot[j] += qv[e] * __bfloat162float(kvs[0][u0 + j][lane * PER + e]);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (u0 + j <= t) {
+          dot[j] *= p.scale_log2;
+          M = fmaxf(M, dot[j]);
+          if (lane == 0) lgs[wr][u0 + j] = dot[j];
+        }
+    }
+    float pmax = fmaxf(pm, pm2);
+    for (int i = 64; i < np; i += 32) {
       float ms, ls;
-      load_ml(i + lane, ms, ls);
+      load_ml(wr, i + lane, ms, ls);
       pmax = fmaxf(pmax, ms);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
     M = fmaxf(M, pmax);
     float l = pm != neg_inf() ? ex2(pm - M) * pl : 0.f;
-    for (int i = 32; i < nS + nP; i += 32) {
+    if (pm2 != neg_inf()) l += ex2(pm2 - M) * pl2;
+    for (int i = 64; i < np; i += 32) {
       float ms, ls;
-      load_ml(i + lane, ms, ls);
+      load_ml(wr, i + lane, ms, ls);
       if (ms != neg_inf()) l += ex2(ms - M) * ls;
     }
+    __syncwarp();
+    const float w = lane <= t ? ex2(lgs[wr][lane] - M) : 0.f;  // (t < 16)
+    l += w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncwarp();
-    for (int u = 0; u <= t; ++u) l += ex2(lgs[rl][u] - M);
+    if (lane <= t) lgs[wr][lane] = w;
     if (lane == 0) {
-      rowM[rl] = M;
-      rowL[rl] = l;
-      seg[rl][0] = cs;
-      seg[rl][1] = nS;
-      seg[rl][2] = cp;
-      seg[rl][3] = nP;
-      at[rl][0] = baseS;
-      at[rl][1] = baseP;
+      rowM[wr] = M;
+      rowL[wr] = l;
     }
   }
   __syncthreads();
-  const int rl = tid & (kCombRows - 1), c = tid / kCombRows;  // row, group of four columns
-  if (rl >= rows) return;
-  const int r = r0 + rl, t = r / p.G, jh = r - t * p.G;
-  const float M = rowM[rl];
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = 0; k < RPT; ++k) {
+    const int rl = rl0 + 8 * k;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k + 1 < RPT) fetch(next, rl + 8, 0);  // the next row's, while this one's are added
+    if (rl < rows) {
+      const int nseg = cnt[rl][0] + cnt[rl][1];
+      const float M = rowM[rl];
+      for (int i0 = 0; i0 < nseg; i0 += NB * SG) {
+        if (i0 > 0) fetch(now, rl, i0);
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    const int c0 = seg[rl][2 * part], cnt = seg[rl][2 * part + 1];
-    const size_t height = part ? p.Mpad : KT, unit = height * D;
-    const size_t first = at[rl][part], row = first % unit;
-    const float* po = (part ? p.partp_o : p.parts_o) + (first - row) + row * 4 + static_cast<size_t>(c) * height * 4;
-    const float* pml = (part ? p.partp_ml : p.parts_ml) + (first / unit * height + row) * 4;
-    for (int i0 = 0; i0 < cnt; i0 += 4) {
-      float ml[4];
-      float4 v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + q;
-        ml[q] = neg_inf();
-        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < cnt && split_nonempty(c0 + i, T, p.nctas)) {
-          ml[q] = pml[static_cast<size_t>(i) * 8 * height];
-          v[q] = *reinterpret_cast<const float4*>(po + static_cast<size_t>(i) * 2 * unit);
+        for (int q = 0; q < NB; ++q) {
+          const float w = now.ml[q] != neg_inf() ? ex2(now.ml[q] - M) : 0.f;
+          acc.x += w * now.v[q].x;
+          acc.y += w * now.v[q].y;
+          acc.z += w * now.v[q].z;
+          acc.w += w * now.v[q].w;
         }
       }
+    }
+    if constexpr (SG > 1) {
+      part_sum[sg][rl][c] = acc;
+      __syncthreads();
+      if (sg > 0) return;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float w = ml[q] != neg_inf() ? ex2(ml[q] - M) : 0.f;
-        acc.x += w * v[q].x;
-        acc.y += w * v[q].y;
-        acc.z += w * v[q].z;
-        acc.w += w * v[q].w;
+      for (int j = 1; j < SG; ++j) {
+        const float4 x = part_sum[j][rl][c];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
       }
     }
-  }
-  for (int u = 0; u <= t; ++u) {
-    const float w = ex2(lgs[rl][u] - M);
-    const __nv_bfloat16* v = &kvs[1][u][4 * c];
-    acc.x += w * __bfloat162float(v[0]);
-    acc.y += w * __bfloat162float(v[1]);
-    acc.z += w * __bfloat162float(v[2]);
-    acc.w += w * __bfloat162float(v[3]);
-  }
-  const float inv = 1.f / rowL[rl];
-  *reinterpret_cast<uint2*>(p.out + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + 4 * c) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (p.k_new && jh == 0) {  // append verify row t
-    const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + t);
-    if (slot >= 0) {
-      const size_t dst = (slot * p.Hkv + g) * D + 4 * c;
+    if (k + 1 < RPT) now = next;
+    if (rl >= rows) return;
+    const int r = r0 + rl, t = r / p.G, jh = r - t * p.G;
+    for (int u = 0; u <= t; ++u) {
+      const float w = lgs[rl][u];
+      const uint2 x = *reinterpret_cast<const uint2*>(&kvs[1][u][4 * c]);
+      acc.x += w * __uint_as_float(x.x << 16);
+      acc.y += w * __uint_as_float(x.x & 0xffff0000u);
+      acc.z += w * __uint_as_float(x.y << 16);
+      acc.w += w * __uint_as_float(x.y & 0xffff0000u);
+    }
+    const float inv = 1.f / rowL[rl];
+    *reinterpret_cast<uint2*>(p.out + ((static_cast<size_t>(b) * p.R + t) * p.Hq + g * p.G + jh) * D + 4 * c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (p.k_new && jh == 0 && slots[t] >= 0) {  // append verify row t
+      const size_t dst = (slots[t] * p.Hkv + g) * D + 4 * c;
       *reinterpret_cast<uint2*>(p.K + dst) = *reinterpret_cast<const uint2*>(&kvs[0][t][4 * c]);
       *reinterpret_cast<uint2*>(p.V + dst) = *reinterpret_cast<const uint2*>(&kvs[1][t][4 * c]);
     }
@@ -1087,26 +1294,29 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
 //
 // One item is a tile of 128 keys and up to N members: S^T[keys][members] on the tensor cores
 // (the keys are the M rows, so few members cost little), one KV head at a time into a double
-// buffer; four warps add the heads' tiles in fp32 registers (the tensor core's own sum runs
-// over one head only) and write rows of consecutive positions.
+// buffer, the three parts of the members' queries side by side as columns; four warps add the
+// parts and the heads' tiles in fp32 registers (the tensor core's own sum runs over one part of
+// one head) and write rows of consecutive positions.  A private range has one member: its
+// items bring and multiply the 16 columns an MMA has at least.
 template <int D, int N>
 struct ZCfg {
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_BYTES = KT * 128;
   static constexpr int K_BYTES = KT * D * 2;
-  static constexpr int PART = N * D * 2;
-  static constexpr int STAGE = K_BYTES + 3 * PART;
+  static constexpr int Z_HALF = 3 * N * 128;      // 64 columns of the query parts
+  static constexpr int STAGE = K_BYTES + HALVES * Z_HALF;
   static constexpr int NST = 163840 / STAGE > 6 ? 6 : 163840 / STAGE;
   static constexpr int NBAR = 2 * NST + 6;
-  static constexpr int THREADS = 192;
-  static constexpr uint32_t TMEM_COLS = 2 * N < 32 ? 32 : 2 * N;
+  static constexpr int THREADS = 224;
+  static constexpr uint32_t TMEM_COLS = N == 16 ? 128 : 512;  // two buffers of 3 N columns
+  static constexpr uint32_t COL_B = TMEM_COLS / 2;
   static size_t smem(int meta) { return 1024 + NST * STAGE + NBAR * 8 + 16 + 4 * static_cast<size_t>(meta); }
 };
 
 template <int D, int N>
 __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
     shared_score_kernel(const SharedParams p, const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmZ) {
+                        const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmZ1) {
   using C = ZCfg<D, N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1122,7 +1332,7 @@ __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 32) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -1165,66 +1375,81 @@ __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
       i.ntok = m.nlen[b] - i.tok0;
       i.members = 1;
     }
-    i.cols = (i.members + 15) & ~15;
+    i.cols = x < totS ? N : 16;  // columns of one part
     return i;
   };
-  if (warp == 4) {
-    const int BR = p.box_rows, box = lane / C::HALVES, half = lane % C::HALVES;
-    int u = 0;
+  if (warp == 4 || warp == 6) {
+    // the boxes of a tile dealt out to two warps, one a lane, as in the attention kernel; the halves
+    // of the query parts likewise
+    const int BR = p.box_rows, second = warp == 6 ? 1 : 0;
+    const int e = 2 * lane + second, box = e / C::HALVES, half = e % C::HALVES;
+    int u = 0, st = 0, lap = 0;
     bool ok = true;
     for (int x = blockIdx.x; ok && x < T; x += gridDim.x) {
       const Item it = item(x);
       const int at = it.tile * KT + box * BR;
       const int y = box < KT / BR && at < it.ntok ? box_slot(p, it.row, it.tok0 + at) : -1;
       const int boxes = __popc(__ballot_sync(0xffffffffu, y >= 0));
-      const int zb = it.cols / 16 * 3 * C::HALVES;  // boxes of 16 members of a part, 64 columns
-      for (int g = 0; ok && g < p.Hkv; ++g, ++u) {
-        const int st = u % C::NST;
-        if (lane == 0 && u >= C::NST) ok = mbar_wait_ab(&empty[st], ((u / C::NST) - 1) & 1, p.status, abort);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int g = 0; g < p.Hkv; ++g) {
+        if (lap > 0) ok = warp_wait(&empty[st], (lap - 1) & 1, p.status, abort);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes * BR * 128 + zb * 16 * 128));
+        const uint32_t dst = smem_u32(smem) + st * C::STAGE;
+        const bool z = second < C::HALVES;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes * BR * 128 + (z ? 3 * it.cols * 128 : 0)));
+          if (z)  // the three parts of `cols` members, one after another
+            tma_load_3d(dst + C::K_BYTES + second * C::Z_HALF, it.cols == N ? &tmZ : &tmZ1, g * D + second * 64, it.seq0,
+                        0, &full[st]);
+        }
         __syncwarp();
-        uint8_t* dst = smem + st * C::STAGE;
-        if (y >= 0) tma_load_2d(dst + half * C::HALF_BYTES + box * BR * 128, &tmK, g * D + half * 64, y, &full[st]);
-        for (int e = lane; e < zb; e += 32) {
-          const int h = e % C::HALVES, q = e / C::HALVES, part = q % 3, blk = q / 3;
-          tma_load_2d(dst + C::K_BYTES + part * C::PART + h * (N * 128) + blk * 16 * 128, &tmZ, g * D + h * 64,
-                      part * p.Bpad + it.seq0 + blk * 16, &full[st]);
+        if (y >= 0)
+          tma_load_2d_at(dst + half * C::HALF_BYTES + box * BR * 128, &tmK, g * D + half * 64, y, &full[st]);
+        __syncwarp();
+        ++u;
+        if (++st == C::NST) {
+          st = 0;
+          ++lap;
         }
       }
     }
-    if (lane == 0)
-      for (int i = u > C::NST ? u - C::NST : 0; i < u; ++i) mbar_wait(&full[i % C::NST], (i / C::NST) & 1, p.status);
+    // (as in the attention kernel: no copy is in flight at the end of a normal run)
+    if (!ok && lane == 0) {
+      volatile int never = 0;
+      for (int i = u > C::NST ? u - C::NST : 0; i < u; ++i)
+        mbar_wait_ab(&full[i % C::NST], (i / C::NST) & 1, nullptr, &never, 2000000ull);
+    }
     __syncwarp();
-  } else if (warp == 5 && lane == 0) {
-    int u = 0;
+  } else if (warp == 5) {
+    int u = 0, st = 0;
+    uint32_t par = 0;
     bool ok = true;
-    const uint32_t base = smem_u32(smem);
+    const uint32_t lead = elect_one() ? 1u : 0u;
+    const uint64_t dk = tc_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t dz = tc_desc_sw128(smem_u32(smem) + C::K_BYTES, 16, 1024);
     for (int x = blockIdx.x; ok && x < T; x += gridDim.x) {
       const Item it = item(x);
-      const uint32_t id = tc_idesc_bf16(128, it.cols, 0, 0);
+      const uint32_t id = tc_idesc_bf16(128, 3 * it.cols, 0, 0);
       for (int g = 0; ok && g < p.Hkv; ++g, ++u) {
-        const int st = u % C::NST;
-        ok = mbar_wait_ab(&full[st], (u / C::NST) & 1, p.status, abort) &&
-             (u < 2 || mbar_wait_ab(&s_free[u & 1], ((u - 2) >> 1) & 1, p.status, abort));
+        ok = warp_wait(&full[st], par, p.status, abort) &&
+             (u < 2 || warp_wait(&s_free[u & 1], ((u - 2) >> 1) & 1, p.status, abort));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ka = base + st * C::STAGE, za = ka + C::K_BYTES;
-        // smallest part first: the large sum is rounded into last
+        const uint64_t da = dk + static_cast<uint64_t>(st * (C::STAGE / 16));
+        const uint64_t db = dz + static_cast<uint64_t>(st * (C::STAGE / 16));
 #pragma unroll
-        for (int part = 2; part >= 0; --part)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma(tm + (u & 1) * N, tc_desc_sw128(ka + (kk >> 2) * C::HALF_BYTES + (kk & 3) * 32, 16, 1024),
-                   tc_desc_sw128(za + part * C::PART + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), id,
-                   (part < 2 || kk > 0) ? 1u : 0u);
-        tc_commit(&s_full[u & 1]);
-        tc_commit(&empty[st]);
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_one(lead, tm + (u & 1) * C::COL_B, da + (kk >> 2) * (C::HALF_BYTES / 16) + (kk & 3) * 2,
+                     db + (kk >> 2) * (C::Z_HALF / 16) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
+        tc_commit_one(lead, &s_full[u & 1]);
+        tc_commit_one(lead, &empty[st]);
+        if (++st == C::NST) {
+          st = 0;
+          par ^= 1;
+        }
       }
     }
-    tc_commit(fin);  // every MMA of this thread complete before the CTA tears down
-    mbar_wait(fin, 0, p.status);
+    tc_commit_one(lead, fin);  // every MMA of this thread complete before the CTA tears down
+    warp_wait(fin, 0, p.status, abort);
   } else if (warp < 4) {
     int u = 0;
     const uint32_t tl = tm + (static_cast<uint32_t>(32 * warp) << 16);
@@ -1239,16 +1464,12 @@ __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < N; c += 16) {
           if (c < it.cols) {
-            uint32_t v[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-                "tcgen05.wait::ld.sync.aligned;"
-                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                : "r"(tl + (u & 1) * N + c)
-                : "memory");
+            float v[3][16];
+            const uint32_t at = tl + (u & 1) * C::COL_B + c;
+            tc_ld16x3_sync(at, at + it.cols, at + 2 * it.cols, v);
+            // (the small parts first: the large sum is rounded into last)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc[c + k] += __uint_as_float(v[k]);
+            for (int k = 0; k < 16; ++k) acc[c + k] += v[0][k] + (v[1][k] + v[2][k]);
           }
         }
         tc_fence_before();
@@ -1291,23 +1512,25 @@ struct Launch {
 };
 
 template <int D, int N>
-cudaError_t launch_scores(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmZ, cudaStream_t stream) {
+cudaError_t launch_scores(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmZ,
+                          const CUtensorMap& tmZ1, cudaStream_t stream) {
   using C = ZCfg<D, N>;
   const size_t smem = C::smem(meta_ints(p.B, p.n_groups));
   cudaError_t e = ensure_smem<shared_score_kernel<D, N>>(smem);
   if (e != cudaSuccess) return e;
   Launch z(p.nctas, C::THREADS, smem, stream);
-  return cudaLaunchKernelEx(&z.cfg, shared_score_kernel<D, N>, p, tmK, tmZ);
+  return cudaLaunchKernelEx(&z.cfg, shared_score_kernel<D, N>, p, tmK, tmZ, tmZ1);
 }
 
 template <int D>
 cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                            const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream) {
+                            const CUtensorMap& tmQ, const CUtensorMap& tmZ, const CUtensorMap& tmZ1,
+                            cudaStream_t stream) {
   cudaError_t e;
-  Launch f(p.mask ? 1 + p.B : 1, kPrepThreads, 0, stream);
+  Launch f(p.mask ? 1 + p.B : 1, 1024, 0, stream);
   if ((e = cudaLaunchKernelEx(&f.cfg, shared_prep_kernel, p)) != cudaSuccess) return e;
   if (p.mask) {
-    e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, stream) : launch_scores<D, 64>(p, tmK, tmZ, stream);
+    e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, tmZ1, stream) : launch_scores<D, 64>(p, tmK, tmZ, tmZ1, stream);
     if (e != cudaSuccess) return e;
   }
   using C = SCfg<D>;
@@ -1315,13 +1538,23 @@ cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const
   if ((e = ensure_smem<shared_attn_kernel<D>>(smem)) != cudaSuccess) return e;
   Launch a(p.nctas, C::THREADS, smem, stream);
   if ((e = cudaLaunchKernelEx(&a.cfg, shared_attn_kernel<D>, p, tmK, tmV, tmQ)) != cudaSuccess) return e;
-  Launch c(p.B * p.Hkv * ((p.M + kCombRows - 1) / kCombRows), 2 * D, 0, stream);
-  return cudaLaunchKernelEx(&c.cfg, shared_combine_kernel<D>, p);
+  // rows of a CTA share their staging, but fewer CTAs than SMs leave SMs idle (16 sequences of one
+  // row and 4 heads a KV head: 10.5 us with two rows a CTA, 13.7 with eight; 8 sequences of 7
+  // rows: 17.5 and 13.0)
+  const int bg = p.B * p.Hkv;
+  if (bg * ((p.M + 7) / 8) >= p.nctas) {
+    Launch c(bg * ((p.M + 7) / 8), 2 * D, 0, stream);
+    return cudaLaunchKernelEx(&c.cfg, shared_combine_kernel<D, 8>, p);
+  }
+  Launch c(bg * ((p.M + 1) / 2), 2 * D, 0, stream);
+  return cudaLaunchKernelEx(&c.cfg, shared_combine_kernel<D, 2>, p);
 }
 
 }  // namespace
 
 int shared_meta_ints(int B, int n_groups) { return meta_ints(B, n_groups); }
+
+size_t shared_rec_bytes(int B) { return sizeof(SeqRec) * (static_cast<size_t>(B) + 1); }
 
 int shared_slots(int D, int B, int n_groups, size_t smem_optin) {
   const int n = meta_ints(B, n_groups);
@@ -1329,9 +1562,10 @@ int shared_slots(int D, int B, int n_groups, size_t smem_optin) {
 }
 
 cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream) {
-  return p.D == 64 ? launch_shared_t<64>(p, tmK, tmV, tmQ, tmZ, stream)
-                   : launch_shared_t<128>(p, tmK, tmV, tmQ, tmZ, stream);
+                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, const CUtensorMap& tmZ1,
+                          cudaStream_t stream) {
+  return p.D == 64 ? launch_shared_t<64>(p, tmK, tmV, tmQ, tmZ, tmZ1, stream)
+                   : launch_shared_t<128>(p, tmK, tmV, tmQ, tmZ, tmZ1, stream);
 }
 
 }  // namespace vg

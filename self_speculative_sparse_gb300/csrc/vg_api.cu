@@ -1204,18 +1204,17 @@ namespace {
 // Query rows of a row tile: whole groups of G heads.
 int shared_row_tile(int G) { return kSharedTileKeys / G * G; }
 
-// q as a 3-D tensor [B * R][Hq][D]; a box is 64 columns of the G heads of 128 / G rows, which
-// lands in shared memory as consecutive rows of 128 bytes (128-byte swizzle).
-vg_status encode_query_map(CUtensorMap* map, const void* q, const Shape& s) {
+// bf16 [n2][n1][n0] as a 3-D tensor; a box of 64 x b1 x b2 lands in shared memory as b1 * b2
+// consecutive rows of 128 bytes (128-byte swizzle).
+vg_status encode_map_3d(CUtensorMap* map, const void* base, int64_t n0, int64_t n1, int64_t n2, int b1, int b2) {
   EncodeTiledFn enc;
   const vg_status st = get_encoder(&enc);
   if (st != VG_OK) return st;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.Hq),
-                              static_cast<cuuint64_t>(s.B) * s.R};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D) * 2, static_cast<cuuint64_t>(s.Hq) * s.D * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(s.G), static_cast<cuuint32_t>(kSharedTileKeys / s.G)};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(n0) * 2, static_cast<cuuint64_t>(n0) * n1 * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(VG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -1223,7 +1222,7 @@ vg_status encode_query_map(CUtensorMap* map, const void* q, const Shape& s) {
 }
 
 struct SharedWs {
-  size_t meta, parts_o, parts_ml, partp_o, partp_ml, qsum, total;
+  size_t meta, rec, parts_o, parts_ml, partp_o, partp_ml, qsum, total;
   int64_t items;  // shared and private items at most
 };
 
@@ -1247,6 +1246,7 @@ SharedWs shared_ws(const Shape& s, int n_groups, int sms) {
   const size_t srows = static_cast<size_t>(sms + shared) * 2 * kSharedTileKeys;
   const size_t prows = static_cast<size_t>(sms + priv) * 2 * s.Mpad;
   w.meta = take(static_cast<size_t>(shared_meta_ints(s.B, n_groups)) * 4);
+  w.rec = take(shared_rec_bytes(s.B));
   w.parts_o = take(srows * s.D * 4);
   w.parts_ml = take(srows * 16);
   w.partp_o = take(prows * s.D * 4);
@@ -1308,12 +1308,17 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   if (p.nslots < 4) return fail(VG_ERR_UNSUPPORTED_SHAPE, "too little shared memory for B=%d", s.B);
   p.Bpad = (s.B + 15) & ~15;
   p.qsum = at<__nv_bfloat16>(ws, w.qsum);
-  CUtensorMap tmK, tmV, tmQ, tmZ;
+  CUtensorMap tmK, tmV, tmQ, tmZ, tmZ1;
   if ((st = encode_cache_map(&tmK, cache->K, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
   if ((st = encode_cache_map(&tmV, cache->V, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
-  if ((st = encode_query_map(&tmQ, q, s)) != VG_OK) return st;
-  tmZ = tmK;
-  if (row_mask && (st = encode_cache_map(&tmZ, p.qsum, 3 * p.Bpad, s.Hkv, s.D, 16)) != VG_OK) return st;
+  if ((st = encode_map_3d(&tmQ, q, s.D, s.Hq, static_cast<int64_t>(s.B) * s.R, s.G, kSharedTileKeys / s.G)) != VG_OK)
+    return st;
+  p.nsc = s.B <= 16 ? 16 : 64;
+  tmZ = tmZ1 = tmK;
+  if (row_mask) {
+    if ((st = encode_map_3d(&tmZ, p.qsum, s.Hkv * s.D, p.Bpad, 3, p.nsc, 3)) != VG_OK) return st;
+    if ((st = encode_map_3d(&tmZ1, p.qsum, s.Hkv * s.D, p.Bpad, 3, 16, 3)) != VG_OK) return st;
+  }
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
   p.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -1342,9 +1347,9 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   p.scale = s.scale;
   p.scale_log2 = s.scale * 1.4426950408889634f;
   p.mask = row_mask;
-  p.nsc = s.B <= 16 ? 16 : 64;
   p.nctas = di.sms;
   p.meta = at<int32_t>(ws, w.meta);
+  p.rec = at<int32_t>(ws, w.rec);
   p.parts_o = at<float>(ws, w.parts_o);
   p.parts_ml = at<float>(ws, w.parts_ml);
   p.partp_o = at<float>(ws, w.partp_o);
@@ -1353,7 +1358,7 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   p.score_stride = score_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.status = dev_status;
-  const cudaError_t e = launch_shared(p, tmK, tmV, tmQ, tmZ, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_shared(p, tmK, tmV, tmQ, tmZ, tmZ1, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "shared verify launch");
   return VG_OK;
 }

@@ -142,6 +142,7 @@ struct SharedParams {
   int nctas, nslots;           // attention grid; ring slots of a CTA
   // workspace
   int32_t* meta;         // the batch's layout (shared_meta_ints)
+  int32_t* rec;          // the same by sequence (shared_rec_bytes)
   float* parts_o;        // [nctas + shared items][2][D / 4][128][4] unnormalised partial outputs
   float* parts_ml;       // [nctas + shared items][2][128][4] max in use (log2 units), sums of both halves of the keys
   float* partp_o;        // [nctas + private items][2][D / 4][Mpad][4]
@@ -235,11 +236,13 @@ int accept_tiles(int V);   // tiles of the sampling draw over a row of V entries
 // Warps of the draft step's combine kernel (4, 8 or 16 from the most partials a
 // sequence has), or 0 when every sequence's entries sit in one CTA (no combine runs).
 int draft_combine_warps(int B, int slots, int nctas);
-// tmQ: q as [B * R][Hq][D], boxes of 64 columns x G heads x 128 / G rows; tmZ: qsum as rows of
-// Hkv * D, boxes of 64 columns x 16 rows (unused without scores)
+// tmQ: q as [B * R][Hq][D], boxes of 64 columns x G heads x 128 / G rows; tmZ, tmZ1: qsum as
+// [3][Bpad][Hkv * D], boxes of 64 columns x nsc or 16 sequences x 3 parts (unused without scores)
 cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, cudaStream_t stream);
+                          const CUtensorMap& tmQ, const CUtensorMap& tmZ, const CUtensorMap& tmZ1,
+                          cudaStream_t stream);
 int shared_meta_ints(int B, int n_groups);
+size_t shared_rec_bytes(int B);
 int shared_slots(int D, int B, int n_groups, size_t smem_optin);  // ring slots that fit a CTA
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream);
 // Grow, cut or fork rows (p.copies: then the copies of a fork's partial pages too).
