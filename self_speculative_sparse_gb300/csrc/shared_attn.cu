@@ -1305,10 +1305,10 @@ struct ZCfg {
   static constexpr int K_BYTES = KT * D * 2;
   static constexpr int Z_HALF = 3 * N * 128;      // 64 columns of the query parts
   static constexpr int STAGE = K_BYTES + HALVES * Z_HALF;
-  static constexpr int NST = 163840 / STAGE > 6 ? 6 : 163840 / STAGE;
+  static constexpr int NST = 196608 / STAGE > 6 ? 6 : 196608 / STAGE;
   static constexpr int NBAR = 2 * NST + 6;
   static constexpr int THREADS = 224;
-  static constexpr uint32_t TMEM_COLS = N == 16 ? 128 : 512;  // two buffers of 3 N columns
+  static constexpr uint32_t TMEM_COLS = N == 16 ? 128 : 256;  // two buffers of 3 N columns
   static constexpr uint32_t COL_B = TMEM_COLS / 2;
   static size_t smem(int meta) { return 1024 + NST * STAGE + NBAR * 8 + 16 + 4 * static_cast<size_t>(meta); }
 };
@@ -1478,11 +1478,12 @@ __global__ void __launch_bounds__(ZCfg<D, N>::THREADS, 1)
       }
       const int at = it.tile * KT + 32 * warp + lane;
       if (at < it.ntok) {
-        float* dst = p.scores + it.tok0 + at;
+        float* dst = p.scores + it.seq0 * p.score_stride + it.tok0 + at;
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (k < it.members && m.nlen[it.seq0 + k] >= 0)
-            dst[static_cast<size_t>(it.seq0 + k) * p.score_stride] = acc[k] * p.scale;
+        for (int k = 0; k < N; ++k) {
+          if (k < it.members) *dst = acc[k] * p.scale;
+          dst += p.score_stride;
+        }
       }
     }
   }
@@ -1530,7 +1531,7 @@ cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const
   Launch f(p.mask ? 1 + p.B : 1, 1024, 0, stream);
   if ((e = cudaLaunchKernelEx(&f.cfg, shared_prep_kernel, p)) != cudaSuccess) return e;
   if (p.mask) {
-    e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, tmZ1, stream) : launch_scores<D, 64>(p, tmK, tmZ, tmZ1, stream);
+    e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, tmZ1, stream) : launch_scores<D, 32>(p, tmK, tmZ, tmZ1, stream);
     if (e != cudaSuccess) return e;
   }
   using C = SCfg<D>;

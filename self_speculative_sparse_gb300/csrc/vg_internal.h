@@ -137,7 +137,7 @@ struct SharedParams {
   int max_len;
   float scale, scale_log2;
   uint32_t mask;               // verify rows summed into scores (0: no scores)
-  int nsc;                     // members of one score item: 16 or 64
+  int nsc;                     // members of one score item: 16 or 32
   int Bpad;                    // rows of one part of qsum: B rounded up to 16
   int nctas, nslots;           // attention grid; ring slots of a CTA
   // workspace
