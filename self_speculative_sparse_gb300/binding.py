@@ -164,10 +164,27 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current stream of the current device.  torch.cuda.current_stream() builds two objects
+    for it (3 us of a call's 9 on the host); its raw form is used where torch has it."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        C = torch._C
+        if hasattr(C, "_cuda_getCurrentRawStream") and hasattr(C, "_cuda_getDevice"):
+            torch.cuda.current_stream()  # (initialises CUDA)
+            _raw_stream = lambda: C._cuda_getCurrentRawStream(C._cuda_getDevice())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
