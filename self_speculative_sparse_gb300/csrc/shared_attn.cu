@@ -423,7 +423,7 @@ struct SCfg {
   static constexpr int HALF_BYTES = KT * 128;     // 64 columns of a tile
   static constexpr int TILE_BYTES = KT * D * 2;   // a K or V tile, or a lane's Q
   static constexpr int OFF_RING = 2 * TILE_BYTES;
-  static constexpr int NBAR = 2 * kMaxSlots + 14;  // full, empty, then s_full, p_full, q_full, o_full, q_empty, fin [2]
+  static constexpr int NBAR = 2 * kMaxSlots + 14;  // full, empty, then s_full, p_full, q_full, o_full, q_empty, fin, turn [2]
   static constexpr int TAIL = NBAR * 8 + 16;
   static constexpr int THREADS = 20 * 32;
   static constexpr uint32_t TMEM_COLS = 512;      // S of the lanes at 0 and 128, O at 256 and 256 + D
@@ -625,6 +625,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
   uint64_t* o_full = s_full + 6;
   uint64_t* q_empty = s_full + 8;
   uint64_t* fin = s_full + 10;
+  uint64_t* turn = s_full + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + C::NBAR);
   // Raised by the first wait that runs out; every later wait then gives up at once.
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -644,6 +645,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       mbar_init(&q_empty[w], 1);
       mbar_init(&o_full[w], 1);
       mbar_init(&fin[w], 1);
+      mbar_init(&turn[w], 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     const uint32_t ts = tm + w * 128, to = tm + C::COL_O + w * D;
     const uint32_t lead = elect_one() ? 1u : 0u;
     int st = 0, lap = 0;  // ring slot of the next use, its lap
-    uint32_t qpar = 0, ppar = 0;
+    uint32_t qpar = 0, ppar = 0, tpar = 0;
     bool ok = true, sole = false;  // sole: this lane is its slots' only reader
     auto skip = [&](int n) {
       st += n;
@@ -845,6 +847,11 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       if (!(ok = ok && have(0))) break;
       qk(last == 0);
       skip(sole ? 2 - w : 1);
+      // The lanes take turns: a lane issues P V and the next Q K^T together, lane 0 first.  Left to
+      // themselves the two issuers' products mix, both lanes' S come late and at the same time, and
+      // the tensor cores wait while both are in their softmax
+      const bool turns = mode != kSingle;
+      if (turns && w == 1 && lane == 0) mbar_arrive(&turn[0]);
       for (int n = 0; n <= last; ++n) {
         const bool end = n == last;
         const int theirs = sole ? (end ? 1 : 2) : 0;
@@ -853,12 +860,17 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         ok = have(0) && (end || have(1)) && warp_wait(&p_full[w], ppar, p.status, abort);
         if (!ok) break;
         ppar ^= 1;
+        if (turns) {
+          if (!(ok = warp_wait(&turn[w], tpar, p.status, abort))) break;
+          tpar ^= 1;
+        }
         pv(n == 0, end);
         skip(1);
         if (!end) {
           qk(n + 1 == last);
           skip(1);
         }
+        if (turns && lane == 0 && (w == 0 || !end)) mbar_arrive(&turn[w ^ 1]);
         if (!w) skip(theirs);
       }
      }
