@@ -856,14 +856,13 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         const bool end = n == last;
         const int theirs = sole ? (end ? 1 : 2) : 0;
         if (w) skip(theirs);
-        // V(n) and K(n + 1) are awaited before P, whose arrival is what the products wait for
-        ok = have(0) && (end || have(1)) && warp_wait(&p_full[w], ppar, p.status, abort);
+        // V(n), K(n + 1) and the turn are awaited before P, whose arrival is what the products wait
+        // for
+        ok = have(0) && (end || have(1)) && (!turns || warp_wait(&turn[w], tpar, p.status, abort)) &&
+             warp_wait(&p_full[w], ppar, p.status, abort);
         if (!ok) break;
+        tpar ^= turns;
         ppar ^= 1;
-        if (turns) {
-          if (!(ok = warp_wait(&turn[w], tpar, p.status, abort))) break;
-          tpar ^= 1;
-        }
         pv(n == 0, end);
         skip(1);
         if (!end) {
