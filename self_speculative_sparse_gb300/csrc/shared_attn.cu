@@ -312,14 +312,24 @@ enum RunMode { kPair, kHeads, kSingle };
 struct Run {
   int mode;
   int tile0, ntiles;  // key tiles of the item's range
-  int row;            // sequence whose tokens locate the keys
+  int row;            // the unit's first sequence, whose tokens locate the keys
   int tok0, ntok;     // first token of the range, tokens in it
-  int seq0, rows;     // first sequence and number of query rows of the unit
+  int rows;           // query rows of the unit
   int head[2];        // KV head of each lane
   int r0[2];          // first query row of each lane
   bool priv;
   int item;           // index of its partials among the shared / private items
 };
+
+// A run as the planner leaves it in shared memory, in a ring of kRuns.
+constexpr int kRuns = 4;
+struct __align__(16) RunRec {
+  int mode, ntiles, tile0, ntok;  // ntiles -1: no further run
+  int tok0, row, rows, priv;
+  int head[2], r0[2];
+  int unit, pad[3];  // of its partials (for lane 0)
+};
+static_assert(sizeof(RunRec) == 64, "");
 
 // The split of the shared (part 0) or private steps: T steps over nc CTAs, as many as have one;
 // the part's step x is step x + first of them.
@@ -364,7 +374,7 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     off = x - m.stepS[g];
     const int it = off / len;
     off -= it * len;
-    r.row = r.seq0 = m.gs[g];
+    r.row = m.gs[g];
     r.rows = members * p.M;
     r.tok0 = 0;
     r.ntok = m.eff[g];
@@ -390,7 +400,7 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     off = x - m.stepP[b];
     const int hp = off / len;
     off -= hp * len;
-    r.row = r.seq0 = b;
+    r.row = b;
     r.rows = p.M;
     r.tok0 = eff;
     r.ntok = m.nlen[b] - eff;
@@ -423,8 +433,10 @@ struct SCfg {
   static constexpr int HALF_BYTES = KT * 128;     // 64 columns of a tile
   static constexpr int TILE_BYTES = KT * D * 2;   // a K or V tile, or a lane's Q
   static constexpr int OFF_RING = 2 * TILE_BYTES;
-  static constexpr int NBAR = 2 * kMaxSlots + 14;  // full, empty, then s_full, p_full, q_full, o_full, q_empty, fin, turn [2]
-  static constexpr int TAIL = NBAR * 8 + 16;
+  // full, empty, then s_full, p_full, q_full, o_full, q_empty, fin, turn [2], run_full, run_empty [kRuns]
+  static constexpr int NBAR = 2 * kMaxSlots + 14 + 2 * kRuns;
+  static constexpr int TAIL = NBAR * 8 + 16 + kRuns * static_cast<int>(sizeof(RunRec));
+  static_assert(NBAR % 2 == 0, "the records are 16-byte aligned");
   static constexpr int THREADS = 20 * 32;
   static constexpr uint32_t TMEM_COLS = 512;      // S of the lanes at 0 and 128, O at 256 and 256 + D
   static constexpr uint32_t COL_O = 256;
@@ -468,6 +480,18 @@ __device__ __forceinline__ void tc_ld64_sync(uint32_t taddr, float (&v)[64]) {
 // Bit patterns to 32 columns of this thread's lane.
 __device__ __forceinline__ void tc_st32b(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+// One fp32 value to a column of this thread's lane, and from one (waited for).
+__device__ __forceinline__ void tc_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ float tc_ld1_sync(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
+  return __uint_as_float(r);
 }
 // Named barrier of n threads that returns whether any of them brought `v`.
 __device__ __forceinline__ bool named_bar_or(int id, int n, bool v) {
@@ -626,11 +650,13 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
   uint64_t* q_empty = s_full + 8;
   uint64_t* fin = s_full + 10;
   uint64_t* turn = s_full + 12;
+  uint64_t* run_full = s_full + 14;
+  uint64_t* run_empty = run_full + kRuns;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + C::NBAR);
   // Raised by the first wait that runs out; every later wait then gives up at once.
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* mbase = reinterpret_cast<int*>(tmem_slot + 4);
-  const Meta m = meta_at(mbase, p.B, p.n_groups);
+  RunRec* recs = reinterpret_cast<RunRec*>(tmem_slot + 4);
+  int* mbase = reinterpret_cast<int*>(recs + kRuns);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 32) {
@@ -647,6 +673,10 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       mbar_init(&fin[w], 1);
       mbar_init(&turn[w], 1);
     }
+    for (int k = 0; k < kRuns; ++k) {
+      mbar_init(&run_full[k], 1);
+      mbar_init(&run_empty[k], 20);
+    }
     *abort = 0;
     fence_mbar_init();
   }
@@ -662,16 +692,56 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     __syncthreads();
     pdl_launch_dependents();
   };
+  // The CTA's run number k (nullptr: no more, or a wait gave up), held until the warp lets it go.
+  auto run_at = [&](int k) -> const RunRec* {
+    const RunRec* r = recs + k % kRuns;
+    return warp_wait(&run_full[k % kRuns], (k / kRuns) & 1, p.status, abort) && r->ntiles >= 0 ? r : nullptr;
+  };
+  auto run_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&run_empty[k % kRuns]);
+  };
 
   if (warp == 16 || warp == 18) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
     begin();
     // ---------------------------------------------------------------- TMA producers
     // A tile is 128 / box_rows boxes (page pieces) of 64 columns: one box a lane, the boxes of
     // every tile dealt out to two warps in turn (a warp issues its lanes' boxes one by one).
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
+    // Warp 16 also finds the CTA's runs, each while the copies of the one before are on their way, and
+    // leaves them in shared memory (each of the 20 warps for itself took 3000 cycles a run, most
+    // of it for instructions out of cache).
+    const Meta m = meta_at(mbase, p.B, p.n_groups);
+    int pass = -1, x = 0, x1 = 0, cta = 0, planned = 0;
+    auto plan = [&] {
+      if (pass == 2) return true;
+      RunRec out{kPair, -1, 0, 0, 0, 0, 0, 0, {0, 0}, {0, 0}, 0, {0, 0, 0}};
+      while (out.ntiles <= 0) {
+        if (x >= x1) {
+          if (++pass == 2) break;
+          x = my_steps(p, m, part_of(m, pass), x1, cta);
+          continue;
+        }
+        const Run r = make_run(p, m, part_of(m, pass), x, x1);
+        out = RunRec{r.mode, r.ntiles, r.tile0, r.ntok, r.tok0, r.row, r.rows, r.priv, {r.head[0], r.head[1]},
+                     {r.r0[0], r.r0[1]}, (cta + r.item) * 2, {0, 0, 0}};
+      }
+      if (pass == 2) out.ntiles = -1;
+      if (planned >= kRuns &&
+          !warp_wait(&run_empty[planned % kRuns], (planned / kRuns - 1) & 1, p.status, abort))
+        return false;
+      if (lane == 0) {
+        recs[planned % kRuns] = out;
+        mbar_arrive(&run_full[planned % kRuns]);
+      }
+      __syncwarp();
+      ++planned;
+      return true;
+    };
     const int BR = p.box_rows;
     const int e = 2 * lane + (warp == 18 ? 1 : 0);
     const int box = e / C::HALVES, half = e % C::HALVES;
@@ -703,11 +773,13 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     };
     const int lw = warp == 18 ? 1 : 0;  // this warp brings the query tiles of that lane
     uint32_t qpar = 1;                  // (the first wait passes)
-    for (int pass = 0; pass < 2; ++pass) {
-     int x1, cta;
-     for (int x = my_steps(p, m, part_of(m, pass), x1, cta); ok && x < x1;) {
-      const Run r = make_run(p, m, part_of(m, pass), x, x1);
-      if (r.ntiles == 0) continue;
+    if (lw == 0) ok = plan();
+    for (int k = 0; ok; ++k) {
+      const RunRec* rec = run_at(k);
+      if (!rec) break;
+      const RunRec r = *rec;
+      const int r0 = lw ? r.r0[1] : r.r0[0], my_head = lw ? r.head[1] : r.head[0];
+      run_done(k);
       // page-table word of this lane's box in tile n, loaded a tile ahead; its slot row (-1: no
       // box, or reported) when the tile is issued
       auto word = [&](int n) {
@@ -736,8 +808,8 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           mbar_arrive_expect_tx(&q_full[lw], static_cast<uint32_t>(p.RT * 128 * C::HALVES));
 #pragma unroll
           for (int h = 0; h < C::HALVES; ++h)
-            tma_load_3d(smem_u32(smem) + lw * C::TILE_BYTES + h * C::HALF_BYTES, &tmQ, h * 64, r.head[lw] * p.G,
-                        r.seq0 * p.R + r.r0[lw] / p.G, &q_full[lw]);
+            tma_load_3d(smem_u32(smem) + lw * C::TILE_BYTES + h * C::HALF_BYTES, &tmQ, h * 64, my_head * p.G,
+                        r.row * p.R + r0 / p.G, &q_full[lw]);
         }
         __syncwarp();
       }
@@ -756,9 +828,9 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         }
         y = yn;
         w1 = w2;
+        if (ok && n == 0 && lw == 0) ok = plan();
       }
-      zeros |= r.priv;
-     }
+      zeros |= r.priv != 0;
     }
     // No copy may still be in flight when the CTA exits: normally the issuers have waited
     // for every one; after a lost wait the last ones issued here get 2 ms each to land.
@@ -823,12 +895,11 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       const int s2 = st + ahead < NS ? st + ahead : st + ahead - NS;
       return filled(full, empty, s2, st + ahead < NS ? lap : lap + 1, p.status, abort);
     };
-    for (int pass = 0; pass < 2; ++pass) {
-     int x1, cta;
-     for (int x = my_steps(p, m, part_of(m, pass), x1, cta); ok && x < x1;) {
-      const Run r = make_run(p, m, part_of(m, pass), x, x1);
-      const int ntiles = __shfl_sync(0xffffffffu, r.ntiles, 0), mode = __shfl_sync(0xffffffffu, r.mode, 0);
-      if (ntiles == 0) continue;
+    for (int k = 0; ok; ++k) {
+      const RunRec* rec = run_at(k);
+      if (!rec) break;
+      const int ntiles = __shfl_sync(0xffffffffu, rec->ntiles, 0), mode = __shfl_sync(0xffffffffu, rec->mode, 0);
+      run_done(k);
       const int last = ntiles - 1;
       if (mode == kSingle && w == 1) {
         for (int i = 0; ok && i < 2 * ntiles; ++i) {
@@ -872,7 +943,6 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         if (turns && lane == 0 && (w == 0 || !end)) mbar_arrive(&turn[w ^ 1]);
         if (!w) skip(theirs);
       }
-     }
     }
     tc_commit_one(lead, &fin[w]);  // every MMA of this thread complete before the CTA tears down
     warp_wait(&fin[w], 0, p.status, abort);
@@ -889,41 +959,39 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     const uint32_t tq = tm + (static_cast<uint32_t>(32 * quad) << 16);
     const uint32_t ts = tq + w * 128, to = tq + C::COL_O + w * D + half * (D / 2);
     const float c2 = p.scale_log2;
+    const uint32_t to_mine = to, to_other = tq + C::COL_O + w * D + (half ^ 1) * (D / 2);
     int base = 0, ns = 0, nr = 0;  // ring uses, tiles and runs of this lane so far
-    // Pass -1 runs a tile of whatever tensor memory holds through the code, without a wait, an
+    // Run -1 takes a tile of whatever tensor memory holds through the code, without a wait, an
     // arrival or a store, while the previous kernel ends and the first tiles are on their way:
     // the first real tile then finds its instructions in the caches (it took 11,000 cycles to
     // go from S to P without that, of a decode step's 75,000).
-    for (int pass = -1; pass < 2; ++pass) {
-     const bool real = pass >= 0;
-     int x = 0, x1 = 1, cta = 0;
-     if (pass == 0) begin();
-     if (real) x = my_steps(p, m, part_of(m, pass), x1, cta);
-     while (x < x1) {
-      Run r;
+    for (int k = -1;; ++k) {
+      const bool real = k >= 0;
+      if (k == 0) begin();
+      const RunRec* rec = recs;
+      int mode = kPair, last = 0, keys = KT, nrows = KT;
       if (real) {
-        r = make_run(p, m, part_of(m, pass), x, x1);
-      } else {
-        r = Run{kPair, 0, 1, 0, 0, KT, 0, 2 * KT, {0, 0}, {0, 0}, false, 0};
-        x = x1;
+        if (!(rec = run_at(k))) break;
+        mode = rec->mode;
+        last = rec->ntiles - 1;
+        keys = rec->ntok - rec->tile0 * KT;
+        nrows = min(p.RT, rec->rows - rec->r0[w]);
+        if (mode == kSingle && w == 1) {
+          base += run_uses(mode, last + 1);
+          run_done(k);
+          continue;
+        }
       }
-      if (r.ntiles == 0) continue;
-      if (r.mode == kSingle && w == 1) {
-        base += run_uses(r.mode, r.ntiles);
-        continue;
-      }
-      const int last = r.ntiles - 1;
-      const int nrows = min(p.RT, r.rows - r.r0[w]);
       const bool live = 32 * quad < nrows;  // (a warp without rows only keeps the barriers' count)
       float mx = neg_inf(), l = 0.f;        // the maximum in use (log2 units), this half's sum
-      for (int n = 0; n < r.ntiles; ++n) {
-        const int left = r.ntok - (r.tile0 + n) * KT;  // keys of the tile (128 or more: all)
+      for (int n = 0; n <= last; ++n) {
+        const int left = keys - n * KT;  // keys of the tile (128 or more: all)
         if (real) warp_wait(&s_full[w], ns++ & 1, p.status, abort);
         tc_fence_after();
         if (left < KT) {
           // value rows past the range hold whatever was there: zeroed, so that 0 * V is 0 (after
           // the wait for S, which orders this tile's V within NS uses of its K: see filled)
-          const int use = base + v_use(r.mode, w, n, last);
+          const int use = base + v_use(mode, w, n, last);
           filled(full, empty, use % NS, use / NS, p.status, abort);
           uint8_t* vt = ring + static_cast<size_t>(use % NS) * C::TILE_BYTES;
           for (int e = threadIdx.x & 255; e < C::HALVES * KT * 8; e += 256) {
@@ -941,55 +1009,73 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         const int valid = left - HK * half;  // keys of this half (64 or more: all)
         uint32_t pk[HK / 2];
         float ls;
-        for (bool known = n > 0;; known = true) {
-          if (known) {
-            // P = 2^(s c2 - mx) of this half, its sum (of the fp32 values: a packed add) and maximum
-            float s[HK];
-            tc_ld64_sync(ts + HK * half, s);
-            if (valid < HK) {
+        auto load_s = [&](float (&s)[HK]) {
+          tc_ld64_sync(ts + HK * half, s);
+          if (valid < HK) {
 #pragma unroll
-              for (int k = 0; k < HK; ++k)
-                if (k >= valid) s[k] = neg_inf();
-            }
-            float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            float t2[2] = {s[0], s[1]};
-#pragma unroll
-            for (int k = 0; k < HK; k += 2) {
-              t2[(k >> 1) & 1] = max3(t2[(k >> 1) & 1], s[k], s[k + 1]);
-              const float2 e = fma2(make_float2(s[k], s[k + 1]), make_float2(c2, c2), make_float2(-mx, -mx));
-              const float2 w2 = make_float2(ex2(e.x), ex2(e.y));
-              a2[(k >> 1) & 1] = add2(a2[(k >> 1) & 1], w2);
-              pk[k / 2] = pack_bf16(w2.x, w2.y);
-            }
-            ls = (a2[0].x + a2[0].y) + (a2[1].x + a2[1].y);
-            // (both threads of each row have read S after the barrier: P may overwrite it)
-            if (!named_bar_or(pair_bar, 64, row < nrows && fmaxf(t2[0], t2[1]) * c2 > mx + kRescaleSlack)) break;
+            for (int i = 0; i < HK; ++i)
+              if (i >= valid) s[i] = neg_inf();
           }
-          // rare, and each run's first tile: the row's maximum over the whole tile, which both
-          // threads of the row read for themselves, becomes the one in use; then (again) P
+        };
+        if (n == 0) {
+          // The run's first tile gives the maximum to begin with.  The row's two threads tell each
+          // other their half's through the first column of their half of O, which is read out and
+          // not yet written again
+          float s[HK];
+          load_s(s);
+          float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 0; i < HK; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], s[i + 2 * j], s[i + 2 * j + 1]);
+          const float t = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]) * c2;
+          tc_st1(to_mine, t);
+          tc_wait_st();
+          tc_fence_before();
+          named_bar_or(pair_bar, 64, false);
+          tc_fence_after();
+          mx = fmaxf(t, tc_ld1_sync(to_other));
+        }
+        while (true) {
+          // P = 2^(s c2 - mx) of this half, its sum (of the fp32 values: a packed add) and maximum
+          float s[HK];
+          load_s(s);
+          float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float t2[2] = {s[0], s[1]};
+#pragma unroll
+          for (int i = 0; i < HK; i += 2) {
+            t2[(i >> 1) & 1] = max3(t2[(i >> 1) & 1], s[i], s[i + 1]);
+            const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c2, c2), make_float2(-mx, -mx));
+            const float2 w2 = make_float2(ex2(e.x), ex2(e.y));
+            a2[(i >> 1) & 1] = add2(a2[(i >> 1) & 1], w2);
+            pk[i / 2] = pack_bf16(w2.x, w2.y);
+          }
+          ls = (a2[0].x + a2[0].y) + (a2[1].x + a2[1].y);
+          // (both threads of each row have read S after the barrier: P may overwrite it)
+          if (!named_bar_or(pair_bar, 64, row < nrows && fmaxf(t2[0], t2[1]) * c2 > mx + kRescaleSlack)) break;
+          // rare: the row's maximum over the whole tile, which both threads of the row read for
+          // themselves, becomes the one in use; then P again
           float t = neg_inf();
 #pragma unroll 1
           for (int c0 = 0; c0 < KT; c0 += 32) {
             float v[32];
             tc_ld32_sync(ts + c0, v);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) t = fmaxf(t, c0 + k < left ? v[k] : neg_inf());
+            for (int i = 0; i < 32; ++i) t = fmaxf(t, c0 + i < left ? v[i] : neg_inf());
           }
           t *= c2;
-          const float mn = n == 0 || t > mx + kRescaleSlack ? fmaxf(mx, t) : mx;
-          if (n > 0) {
-            // (P V of the lane's previous tile has completed: the commit that brought this S
-            // came after it)
-            const float alpha = mn != mx ? ex2(mx - mn) : 1.f;
-            l *= alpha;
+          const float mn = t > mx + kRescaleSlack ? t : mx;
+          // (P V of the lane's previous tile has completed: the commit that brought this S
+          // came after it)
+          const float alpha = mn != mx ? ex2(mx - mn) : 1.f;
+          l *= alpha;
 #pragma unroll 1
-            for (int c0 = 0; c0 < D / 2; c0 += 32) {
-              float o[32];
-              tc_ld32_sync(to + c0, o);
+          for (int c0 = 0; c0 < D / 2; c0 += 32) {
+            float o[32];
+            tc_ld32_sync(to + c0, o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= alpha;
-              tc_st32(to + c0, o);
-            }
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tc_st32(to + c0, o);
           }
           mx = mn;
         }
@@ -1002,37 +1088,38 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         __syncwarp();
         if (real && lane == 0) mbar_arrive(&p_full[w]);
       }
-      if (!real) break;
+      if (!real) continue;
       // the run's partial: (O, max, sum) of each row once P V of its last tile has landed
       warp_wait(&o_full[w], nr & 1, p.status, abort);
       ++nr;
       tc_fence_after();
       if (live) {
         // four columns of 32 rows lie together: a warp's stores are 512 contiguous bytes
-        const int height = r.priv ? p.Mpad : KT;
-        const size_t unit = static_cast<size_t>(cta + r.item) * 2 + w;
-        float* po = (r.priv ? p.partp_o : p.parts_o) + (unit * D + half * (D / 2)) * height + row * 4;
+        const bool priv = rec->priv != 0;
+        const int height = priv ? p.Mpad : KT;
+        const size_t unit = static_cast<size_t>(rec->unit + w);
+        float* po = (priv ? p.partp_o : p.parts_o) + (unit * D + half * (D / 2)) * height + row * 4;
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
           float o[32];
           tc_ld32_sync(to + c0, o);
           if (row < nrows) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(po + static_cast<size_t>(c0 + k) * height) =
-                  make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(po + static_cast<size_t>(c0 + i) * height) =
+                  make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         // (max, sum of each half of the keys, unused)
-        float* pml = (r.priv ? p.partp_ml : p.parts_ml) + (unit * height + row) * 4;
+        float* pml = (priv ? p.partp_ml : p.parts_ml) + (unit * height + row) * 4;
         if (row < nrows) {
           if (half == 0) *reinterpret_cast<float2*>(pml) = make_float2(mx, l);
           else pml[2] = l;
         }
       }
       tc_fence_before();
-      base += run_uses(r.mode, r.ntiles);
-     }
+      base += run_uses(mode, last + 1);
+      run_done(k);
     }
   }
   __syncwarp();
