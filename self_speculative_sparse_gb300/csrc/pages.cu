@@ -223,15 +223,14 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
   }
 }
 
-// The same for up to kSmallRequests requests and a pool of kSmallPages: what the requests ask is held in
-// the shared memory of every CTA, so that only two of the phases need the cluster's barrier and
-// nothing is handed from one to the next through global memory but the counts: (1) every CTA
-// enters all named rows into a hash table (the lowest request of a row wins); a warp a request
-// checks it, gives back its pages and leaves what it asks; (2) every CTA scans the requests, and
-// counts the free pages of its share of the pool, which stay as a mask in registers; (3) the
-// thread of a free page finds the request whose page it becomes by its rank, and writes it
-// there.  A request for 16 rows of a pool of 1024 pages takes 6.3 us so and 11 us with the kernel above;
-// for 512 rows of 262144 pages 10 to 13 us and 16 to 17.
+// The same for up to kSmallRequests requests and a pool of kSmallPages: every CTA has what all the
+// requests ask in its own shared memory, so that two cluster barriers are left, and nothing but the
+// reference counts passes through global memory: (1) a thread a request checks it; a hash table
+// finds the first request that names a row; (2) a warp a request gives back the pages that its
+// row no longer holds; (3) every CTA counts the free pages of its share of the pool, kept as a
+// mask in registers; (4) the thread of a free page finds the request whose page it becomes by
+// its rank, and writes it there.  A request for 16 rows of a pool of 1024 pages takes 6.2 us so
+// and 11 us with the kernel above; for 512 rows of 131072 pages 8 to 12 us and 16 to 17.
 constexpr int kSmallRequests = 1024;
 constexpr int kSmallPages = kPageMaxCluster * kPageThreads * 32;
 constexpr int kHash = 2048;
@@ -241,7 +240,9 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   __shared__ ClusterShared s;
   __shared__ int hash_row[kHash], hash_first[kHash];
-  __shared__ int child[kSmallRequests], have_of[kSmallRequests], need_of[kSmallRequests], start_of[kSmallRequests];
+  __shared__ int child[kSmallRequests], have_of[kSmallRequests], start_of[kSmallRequests];
+  __shared__ int2 give[kSmallRequests];  // entries of its row that a request gives back: first, end
+  int* need_of = hash_row;               // (once the hash table has been read)
   const int tid = threadIdx.x, lane = tid & 31;
   const int gw = (rank * kPageThreads + tid) >> 5, GW = (C * kPageThreads) >> 5;
   for (int i = tid; i < kHash; i += kPageThreads) {
@@ -249,21 +250,25 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
     hash_first[i] = INT_MAX;
   }
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  pdl_wait();
-  int my_child = -1;
-  if (tid < p.n) {
-    my_child = p.seq ? p.seq[tid] : tid;
-    child[tid] = my_child;
-  }
   __syncthreads();
+  pdl_wait();
+  // ---- check the requests
   auto slot_of = [&](int row) { return static_cast<int>((static_cast<uint32_t>(row) * 2654435761u) >> 21); };
-  if (my_child >= 0 && my_child < p.n_seqs) {
-    int h = slot_of(my_child);
-    for (;; h = (h + 1) & (kHash - 1)) {  // (at most half of the entries are taken)
-      const int was = atomicCAS(&hash_row[h], -1, my_child);
-      if (was == -1 || was == my_child) break;
+  int c = -1, f = -1, len = 0, held = 0, fh = 0;
+  if (tid < p.n) {
+    c = p.seq ? p.seq[tid] : tid;
+    len = p.length[tid];
+    f = p.parent ? p.parent[tid] : 0;
+    if (c >= 0 && c < p.n_seqs) {
+      held = p.held[c];
+      int h = slot_of(c);
+      for (;; h = (h + 1) & (kHash - 1)) {  // (at most half of the entries are taken)
+        const int was = atomicCAS(&hash_row[h], -1, c);
+        if (was == -1 || was == c) break;
+      }
+      atomicMin(&hash_first[h], tid);
     }
-    atomicMin(&hash_first[h], tid);
+    if (p.parent && f >= 0 && f < p.n_seqs) fh = p.held[f];
   }
   __syncthreads();
   auto first_of = [&](int row) {  // the first request that names a row, INT_MAX: none
@@ -272,85 +277,105 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
       if (hash_row[h] == -1) return INT_MAX;
     }
   };
-  // ---- check each request, give back what its row no longer holds
-  for (int j = gw; j < p.n; j += GW) {
-    const int c = child[j], len = p.length[j], f = p.parent ? p.parent[j] : 0;
-    bool ok = c >= 0 && c < p.n_seqs && len >= 0 && f >= 0 && f < p.n_seqs;
-    int total = 0, have = 0, held = 0, keep = 0;
+  int need = 0, have = -1;
+  if (tid < p.n) {
+    const int64_t want = (static_cast<int64_t>(len) + p.room + p.page_size - 1) / p.page_size;
+    bool ok = c >= 0 && c < p.n_seqs && len >= 0 && first_of(c) == tid && held >= 0 && held <= p.pages_per_seq &&
+              want <= p.pages_per_seq;
+    if (ok && p.parent)
+      ok = f >= 0 && f < p.n_seqs && first_of(f) == INT_MAX && fh >= 0 && fh <= p.pages_per_seq &&
+           len <= static_cast<int64_t>(fh) * p.page_size;
     if (ok) {
-      held = p.held[c];
-      const int fh = p.parent ? p.held[f] : 0;
-      const int64_t want = (static_cast<int64_t>(len) + p.room + p.page_size - 1) / p.page_size;
-      total = static_cast<int>(want < INT_MAX ? want : INT_MAX);
-      ok = first_of(c) == j && held >= 0 && held <= p.pages_per_seq && want <= p.pages_per_seq;
-      if (p.parent)
-        ok = ok && first_of(f) == INT_MAX && fh >= 0 && fh <= p.pages_per_seq &&
-             len <= static_cast<int64_t>(fh) * p.page_size;
-    }
-    if (ok) {
-      have = p.parent ? len / p.page_size : min(held, total);
-      keep = p.parent ? 0 : have;
-      int32_t* row = p.table + static_cast<int64_t>(c) * p.pages_per_seq;
-      for (int i = keep + lane; i < held; i += 32) {
-        const int pg = row[i];
-        if (pg >= 0 && pg < p.n_pages) atomicSub(p.refs + pg, 1);
-        else report(p.status, VG_ERR_DEVICE_BOUNDS);
-        row[i] = -1;
-      }
-    } else if (lane == 0) {
+      have = p.parent ? len / p.page_size : min(held, static_cast<int>(want));  // whole pages shared, or kept
+      need = static_cast<int>(want) - have;
+    } else if (rank == 0) {
       report(p.status, VG_ERR_DEVICE_BOUNDS);
     }
-    if (lane == 0) {
-      p.need[j] = ok ? total - have : 0;
-      p.have[j] = ok ? have : -1;
+    child[tid] = c;
+    have_of[tid] = have;
+    give[tid] = ok ? make_int2(p.parent ? 0 : have, held) : make_int2(0, 0);
+  }
+  __syncthreads();  // (the hash table has been read)
+  if (tid < p.n) need_of[tid] = need;
+  // ---- give back what the rows no longer hold
+  for (int j = gw; j < p.n; j += GW) {
+    const int2 range = give[j];
+    if (range.x >= range.y) continue;
+    int32_t* row = p.table + static_cast<int64_t>(child[j]) * p.pages_per_seq;
+    for (int i0 = range.x + lane; i0 < range.y; i0 += 128) {
+      int pg[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) pg[u] = i0 + 32 * u < range.y ? row[i0 + 32 * u] : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (i0 + 32 * u >= range.y) break;
+        if (pg[u] >= 0 && pg[u] < p.n_pages) atomicSub(p.refs + pg[u], 1);
+        else report(p.status, VG_ERR_DEVICE_BOUNDS);
+        row[i0 + 32 * u] = -1;
+      }
     }
   }
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory may be written
   cluster.sync();
-  // ---- the requests' places among the pages handed out; the free pages of every CTA's share
-  int lo, hi, needed, mine;
+  // ---- the free pages of every CTA's share (and, while the counts come, the requests' places among
+  // the pages handed out)
+  int lo, hi, mine, needed, start = 0;
   page_run(p.n_pages, rank, C, lo, hi);
-  int need = 0, have = -1;
-  if (tid < p.n) {
-    need = __ldcg(p.need + tid);
-    have = __ldcg(p.have + tid);
-  }
   uint32_t mask = 0;  // free pages of this thread's run (32 at most)
-  for (int i = lo; i < hi; i += 4) {  // (the run starts at a multiple of four)
-    if (i + 4 <= hi) {
-      const int4 v = __ldcg(reinterpret_cast<const int4*>(p.refs + i));
-      mask |= ((v.x <= 0 ? 1u : 0u) | (v.y <= 0 ? 2u : 0u) | (v.z <= 0 ? 4u : 0u) | (v.w <= 0 ? 8u : 0u)) << (i - lo);
-    } else {
-      for (int k = i; k < hi; ++k) mask |= (__ldcg(p.refs + k) <= 0 ? 1u : 0u) << (k - lo);
+  for (int i0 = lo;; i0 += 8) {  // (the run starts at a multiple of four)
+    int4 v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = i0 + 4 * u;
+      v[u] = make_int4(1, 1, 1, 1);
+      if (i + 4 <= hi) {
+        v[u] = __ldcg(reinterpret_cast<const int4*>(p.refs + i));
+      } else {
+        if (i < hi) v[u].x = __ldcg(p.refs + i);
+        if (i + 1 < hi) v[u].y = __ldcg(p.refs + i + 1);
+        if (i + 2 < hi) v[u].z = __ldcg(p.refs + i + 2);
+      }
     }
-  }
-  const int start = block_scan(need, s.sh, &needed);
-  if (tid < p.n) {
-    have_of[tid] = have;
-    need_of[tid] = need;
-    start_of[tid] = start;
+    if (i0 == lo) {
+      start = block_scan(need, s.sh, &needed);
+      if (tid < p.n) start_of[tid] = start;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (i0 + 4 * u < hi)
+        mask |= ((v[u].x <= 0 ? 1u : 0u) | (v[u].y <= 0 ? 2u : 0u) | (v[u].z <= 0 ? 4u : 0u) | (v[u].w <= 0 ? 8u : 0u))
+                << (i0 + 4 * u - lo);
+    if (i0 + 8 >= hi) break;
   }
   const int before = block_scan(__popc(mask), s.sh, &mine);
   if (tid < C) *cluster.map_shared_rank(s.counts + rank, tid) = mine;
   cluster.sync();
   pdl_launch_dependents();
   int base = before, free_all = 0;
-  for (int c = 0; c < C; ++c) {
-    if (c < rank) base += s.counts[c];
-    free_all += s.counts[c];
+  for (int r = 0; r < C; ++r) {
+    if (r < rank) base += s.counts[r];
+    free_all += s.counts[r];
   }
   // ---- the lowest free pages, in order, to the rows that get them.  The request of rank r is the
-  // last one that starts at r or before: it asks for pages, as the one behind it would start there too
+  // last one that starts at r or before (it asks for pages, as the one behind it would start there
+  // too); the next page's is the same or one soon behind it
+  int a = 0, first = 0, end = 0;
+  int32_t* row = nullptr;
   for (; mask != 0 && base < needed; mask &= mask - 1, ++base) {
     const int pg = lo + __ffs(mask) - 1;
-    int a = 0, b = p.n - 1;
-    while (a < b) {
-      const int mid = (a + b + 1) >> 1;
-      if (start_of[mid] <= base) a = mid; else b = mid - 1;
+    if (row == nullptr) {
+      for (int b = p.n - 1; a < b;) {
+        const int mid = (a + b + 1) >> 1;
+        if (start_of[mid] <= base) a = mid; else b = mid - 1;
+      }
     }
-    if (start_of[a] + need_of[a] > free_all) continue;  // not served
-    const int i = base - start_of[a];
-    p.table[static_cast<int64_t>(child[a]) * p.pages_per_seq + have_of[a] + i] = pg;
+    if (base >= end) {
+      while ((end = (first = start_of[a]) + need_of[a]) <= base) ++a;
+      row = p.table + static_cast<int64_t>(child[a]) * p.pages_per_seq + have_of[a];
+    }
+    if (end > free_all) continue;  // not served
+    const int i = base - first;
+    row[i] = pg;
     p.refs[pg] = 1;
     if (i == 0 && p.copies) {
       const int part = p.length[a] % p.page_size;
@@ -365,14 +390,13 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
   // ---- what the rows hold
   if (rank == C - 1 && tid < p.n) {
     const bool served = need == 0 || start + need <= free_all;
-    if (p.copies && (have < 0 || !served || need == 0 || p.length[tid] % p.page_size == 0))
-      p.copies[tid] = make_int4(0, 0, 0, 0);
+    if (p.copies) {
+      if (have < 0 || !served || need == 0 || len % p.page_size == 0) p.copies[tid] = make_int4(0, 0, 0, 0);
+      p.have[tid] = served ? have : -1;
+    }
     if (have >= 0) {
-      if (!served) {
-        report(p.status, VG_ERR_DEVICE_PAGES);
-        if (p.parent) p.have[tid] = -1;
-      }
-      p.held[my_child] = served ? have + need : (p.parent ? 0 : have);
+      if (!served) report(p.status, VG_ERR_DEVICE_PAGES);
+      p.held[c] = served ? have + need : (p.parent ? 0 : have);
     }
   }
 }
