@@ -307,10 +307,16 @@ def vg_sparse_draft_attn_noalloc(dims, cache, q, k_new, v_new, idx, count, k_str
                                                ptr(tail_len), ptr(out), ptr(dev_status), _stream(stream)))
 
 
+def _holding(struct, *tensors):
+    """The struct, keeping the tensors that it points to allocated as long as it lives."""
+    struct.tensors = tensors
+    return struct
+
+
 def make_groups(group_start, shared_len) -> vg_prefix_groups:
     """Groups of consecutive sequences and the tokens each shares: int32 tensors group_start
     [n_groups + 1] (None: one group of the whole batch) and shared_len [n_groups]."""
-    return vg_prefix_groups(shared_len.shape[0], ptr(group_start), ptr(shared_len))
+    return _holding(vg_prefix_groups(shared_len.shape[0], ptr(group_start), ptr(shared_len)), group_start, shared_len)
 
 
 def vg_shared_verify_workspace_size(dims: vg_dims, groups: vg_prefix_groups) -> int:
@@ -349,7 +355,7 @@ def vg_rope_freqs(rot_dim: int, base: float, scaling: int = VG_ROPE_PLAIN, facto
 
 def make_rope(freq, rot_dim: int, layout: int = VG_ROPE_HALF, mscale: float = 0.0) -> vg_rope:
     """The rotation of vg_rope_append; freq: the frequencies on the device (64-bit integers)."""
-    return vg_rope(ptr(freq), rot_dim, layout, mscale)
+    return _holding(vg_rope(ptr(freq), rot_dim, layout, mscale), freq)
 
 
 def vg_rope_append(dims, cache, rope: vg_rope, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows, prefix_len,
@@ -362,14 +368,14 @@ def vg_rope_append(dims, cache, rope: vg_rope, q, q_stride, k, k_stride, v, v_st
 
 def make_pages(page_table, held, refs, page_size: int) -> vg_page_pool:
     """The page pool of int32 tensors page_table [n_seqs][pages_per_seq], held [n_seqs], refs [n_pages]."""
-    return vg_page_pool(ptr(page_table), ptr(held), ptr(refs), page_table.shape[0], page_table.shape[1],
-                        refs.shape[0], page_size)
+    return _holding(vg_page_pool(ptr(page_table), ptr(held), ptr(refs), page_table.shape[0], page_table.shape[1],
+                                 refs.shape[0], page_size), page_table, held, refs)
 
 
 def make_caches(layers):
     """The host array of cache structs that the page calls take, from (K, V) tensors of each
     layer ([capacity_slots][...])."""
-    return (vg_kv_cache * len(layers))(*[make_cache(K, V, None) for K, V in layers])
+    return _holding((vg_kv_cache * len(layers))(*[make_cache(K, V, None) for K, V in layers]), *layers)
 
 
 def vg_pages_workspace_size(pool: vg_page_pool) -> int:

@@ -187,6 +187,25 @@ def test_many_rows_wrap_around_the_grid():
     c.check(c.q_out, before)
 
 
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (64, 32, False), (128, 128, True), (64, 20, True),
+                                         (64, 64, False), (128, 100, False), (64, 6, False)])
+def test_more_rows_than_one_a_cta(d, rot, inter, page):
+    c = Case([1, 700, 0, 3, 513], [7, 63, 4, 0, 2000], Hq=6, Hkv=2, d=d, rot=rot, inter=inter, page=page, pad_rows=9,
+             mscale=0.75)
+    before = c.qkv.clone()
+    c.call()
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    c.check(c.q_out, before)
+    assert (c.q_out[1217:] == 9.0).all()
+    c.call(in_place=True)
+    torch.cuda.synchronize()
+    n = c.Hq * c.d
+    assert torch.equal(c.qkv[:1217, :n], c.q_out[:1217, :n]) and torch.equal(c.qkv[1217:], before[1217:])
+    assert torch.equal(c.qkv[:, n:], before[:, n:])
+
+
 @pytest.mark.parametrize("what", ["prefix", "negative", "page", "table"])
 def test_bad_rows_are_reported_and_the_others_served(what):
     c = Case([2, 2, 2], [10, 20, 30], page=16)

@@ -1,8 +1,9 @@
 """vg_shared_verify_attn on the GPU against the oracle's attention of each sequence by itself.
 
 Tolerances, from the arithmetic: a softmax weight enters the value product as bf16 (half a
-step: 2^-8 of it), its sum being taken over the rounded weights, so an output is off by at
-most 2^-8 (A + |out|), A = sum_i p_i |v_i|, and by 2^-8 |out| for its own rounding; fp32
+step: 2^-8 of it), its sum being taken over the fp32 weights, so an output is off by at
+most 2^-8 A, A = sum_i p_i |v_i|, and by 2^-8 |out| for its own rounding (the bound has
+twice that, which a sum over rounded weights would need); fp32
 logits, exponentials and sums add less than 2^-14 A.  A score is a sum of products of fp32
 queries held in three bf16 parts (2^-24 of each) in fp32 additions, some tens of them one
 after another: at most 2^-18 of the sum of the products' magnitudes.
@@ -307,6 +308,42 @@ def test_captured_and_replayed_with_other_lengths_on_another_stream():
         c.out.fill_(float("nan"))
         g.replay()
         c.check()
+
+
+@pytest.mark.parametrize("scores", [False, True])
+def test_many_sequences_and_many_runs_of_a_cta(scores):
+    # 1024 sequences: every CTA works on a dozen items or more, most of them one or two tiles long
+    lens = [(37 * i) % 150 for i in range(1024)]
+    c = Case([1000, 24], [200, 130], [lens[:1000], lens[1000:]], Hq=4, Hkv=4, d=64, page=8, scores=scores)
+    K0, V0 = c.K.clone(), c.V.clone()
+    c.call()
+    c.check(K0=K0, V0=V0)
+
+
+def test_two_captured_calls_share_a_workspace():
+    a = Case([4, 2], [600, 260], [[0, 10, 200, 300], [5, 600]], gamma=2, append=False, seed=1)
+    b = Case([7], [1000], [[i * 31 for i in range(7)]], gamma=1, append=False, seed=2, scores=False, d=64)
+    if b.ws.numel() > a.ws.numel():
+        a.ws = b.ws
+    else:
+        b.ws = a.ws
+    graphs = []
+    for c in (a, b):
+        c.call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call()
+        graphs.append(g)
+    for c in (a, b):
+        c.out.fill_(float("nan"))
+        if c.scores is not None:
+            c.scores.fill_(7.0)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    a.check()
+    b.check()
 
 
 def test_beside_the_verify_call_it_stands_for():
