@@ -1141,15 +1141,18 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
 // partials).  Then the threads of a column add up: the row's shared partials by CTA, its
 // private ones by CTA, the causal values: a fixed order.
 //
-// What bounds it is instructions, most of them addresses and the short sums (64 sequences x 32 rows
-// x 8 heads: 30 us at 0.7 instructions a cycle and partition; 16 or 32 rows a CTA are no faster).
+// What bounds it is instructions, most of them addresses and the short sums: there are some ten
+// products for each of a row's 128 columns (64 sequences x 32 rows x 8 heads: 28.7 us at 0.7
+// instructions a cycle and partition, whether 4, 5 or 6 CTAs fit an SM; 32 us with 16 rows a CTA, 36
+// with 32.  Without the logits it would take 24 us, without the verify rows' keys and values 25).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParams p) {
   constexpr int PER = D / 32, WARPS = D / 16, CH = D / 8, NT = 2 * D;
   constexpr int SG = ROWS < 8 ? 8 / ROWS : 1;      // threads that share a row's four columns
   constexpr int RPT = ROWS < 8 ? 1 : ROWS / 8;     // rows a thread
   constexpr int NB = ROWS == 2 ? 8 : 4;            // partials in flight a thread
-  __shared__ float lgs[ROWS][16], rowM[ROWS], rowL[ROWS];
+  constexpr int NW = 64;                           // partials of a row whose weights are kept
+  __shared__ float lgs[ROWS][16], rowM[ROWS], rowL[ROWS], wts[ROWS][NW];
   // the row's shared and private partials: how many, and the first one's place in units of 16
   // bytes (of O, then of its row of maximum and sums)
   __shared__ int cnt[ROWS][2];
@@ -1205,44 +1208,39 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
     return i < nS ? reinterpret_cast<const float4*>(p.parts_ml) + (at[rl][1] + static_cast<uint32_t>(i) * (2 * KT))
                   : reinterpret_cast<const float4*>(p.partp_ml) + (at[rl][3] + static_cast<uint32_t>(i - nS) * (2 * p.Mpad));
   };
-  auto o_at = [&](int rl, int i, int nS, int c) {
-    return i < nS ? reinterpret_cast<const float4*>(p.parts_o) +
-                        (at[rl][0] + static_cast<uint32_t>(i) * (2 * KT * D / 4) + c * KT)
-                  : reinterpret_cast<const float4*>(p.partp_o) +
-                        (at[rl][2] + static_cast<uint32_t>(i - nS) * (2 * p.Mpad * (D / 4)) + c * p.Mpad);
+  // a thread's four columns of a row: its partials' places (by number), how many shared and in all
+  struct Row {
+    const float4 *s, *p;
+    int nS, n;
+  };
+  auto row_at = [&](int rl, int c) {
+    Row x{nullptr, nullptr, 0, 0};
+    if (rl < rows) {
+      x.nS = cnt[rl][0];
+      x.n = x.nS + cnt[rl][1];
+      x.s = reinterpret_cast<const float4*>(p.parts_o) + (at[rl][0] + c * KT);
+      x.p = reinterpret_cast<const float4*>(p.partp_o) + (at[rl][2] + c * p.Mpad);
+    }
+    return x;
+  };
+  auto o_at = [&](const Row& x, int i) {
+    return i < x.nS ? x.s + static_cast<size_t>(i) * (2 * KT * D / 4)
+                    : x.p + static_cast<size_t>(static_cast<uint32_t>(i - x.nS) * (2 * p.Mpad * (D / 4)));
   };
   const int rl0 = tid % (ROWS < 8 ? ROWS : 8), sg = ROWS < 8 ? tid / ROWS % SG : 0, c = tid / 8;
   struct Batch {
-    float ml[NB];
     float4 v[NB];
   };
-  auto fetch = [&](Batch& x, int rl, int i0) {  // partials i0 + sg, i0 + sg + SG ... of a row
-    const int nS = rl < rows ? cnt[rl][0] : 0, nseg = rl < rows ? nS + cnt[rl][1] : 0;
+  auto fetch = [&](Batch& x, const Row& row, int i0) {  // partials i0 + sg, i0 + sg + SG ... of a row
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
       const int i = i0 + sg + q * SG;
-      x.ml[q] = neg_inf();
-      x.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < nseg) {
-        x.ml[q] = ml_at(rl, i, nS)->x;
-        x.v[q] = *o_at(rl, i, nS, c);
-      }
+      x.v[q] = i < row.n ? *o_at(row, i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   Batch now, next;
-  fetch(now, rl0, 0);
-  for (int e = tid; e < 2 * 16 * CH; e += NT) {
-    const int which = e / (16 * CH), u = e / CH % 16, cc = e % CH;
-    if (u > tmax) continue;
-    const __nv_bfloat16* fresh = which ? p.v_new : p.k_new;
-    const int64_t slot = slots[u];
-    const __nv_bfloat16* src = fresh ? fresh + ((static_cast<size_t>(b) * p.R + u) * p.Hkv + g) * D
-                                     : (which ? p.V : p.K) + ((slot < 0 ? 0 : slot) * p.Hkv + g) * D;
-    uint4 x = reinterpret_cast<const uint4*>(src)[cc];
-    if (!fresh && slot < 0) x = make_uint4(0u, 0u, 0u, 0u);
-    reinterpret_cast<uint4*>(&kvs[which][u][0])[cc] = x;
-  }
-  __syncthreads();
+  Row here = row_at(rl0, c);
+  fetch(now, here, 0);
   auto load_ml = [&](int rl, int i, float& ms, float& ls) {  // (max, sum) of partial i of a row
     ms = neg_inf();
     ls = 0.f;
@@ -1268,6 +1266,18 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
 #pragma unroll
     for (int e = 0; e < PER / 2; ++e) qrow[k][e] = src[e];
   }
+  for (int e = tid; e < 2 * 16 * CH; e += NT) {
+    const int which = e / (16 * CH), u = e / CH % 16, cc = e % CH;
+    if (u > tmax) continue;
+    const __nv_bfloat16* fresh = which ? p.v_new : p.k_new;
+    const int64_t slot = slots[u];
+    const __nv_bfloat16* src = fresh ? fresh + ((static_cast<size_t>(b) * p.R + u) * p.Hkv + g) * D
+                                     : (which ? p.V : p.K) + ((slot < 0 ? 0 : slot) * p.Hkv + g) * D;
+    uint4 x = reinterpret_cast<const uint4*>(src)[cc];
+    if (!fresh && slot < 0) x = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4*>(&kvs[which][u][0])[cc] = x;
+  }
+  __syncthreads();
 #pragma unroll
   for (int kr = 0; kr < RPW; ++kr) {
     const int wr = warp + kr * WARPS;
@@ -1281,28 +1291,41 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
       qv[2 * e] = __uint_as_float(qrow[kr][e] << 16);
       qv[2 * e + 1] = __uint_as_float(qrow[kr][e] & 0xffff0000u);
     }
-    float M = neg_inf();
-    for (int u0 = 0; u0 <= t; u0 += 4) {  // (four keys at a time: their sums overlap)
-      float dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (u0 + j <= t) {
-#pragma unroll
-          for (int e = 0; e < PER; ++e) dot[j] += qv[e] * __bfloat162float(kvs[0][u0 + j][lane * PER + e]);
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (u0 + j <= t) {
-          dot[j] *= p.scale_log2;
-          M = fmaxf(M, dot[j]);
-          if (lane == 0) lgs[wr][u0 + j] = dot[j];
-        }
-    }
     float pmax = fmaxf(pm, pm2);
+    for (int u0 = 0; u0 <= t; u0 += 8) {
+      // eight keys at a time; their sums over the lanes in nine exchanges, after which lanes 4 j .. 4 j + 3
+      // have key j's
+      float dot[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dot[j] = 0.f;
+        if (u0 + j <= t) {
+#pragma unroll
+          for (int e = 0; e < PER; e += 2) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(&kvs[0][u0 + j][lane * PER + e]);
+            dot[j] += qv[e] * __uint_as_float(x << 16);
+            dot[j] += qv[e + 1] * __uint_as_float(x & 0xffff0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 4; h > 0; h >>= 1)
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+          const bool up = (lane & (4 * h)) != 0;
+          const float keep = up ? dot[j + h] : dot[j], give = up ? dot[j] : dot[j + h];
+          dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
+        }
+      float x = dot[0];
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x *= p.scale_log2;
+      const int u = u0 + (lane >> 2);
+      if (u <= t) {
+        pmax = fmaxf(pmax, x);
+        if ((lane & 3) == 0) lgs[wr][u] = x;
+      }
+    }
     for (int i = 64; i < np; i += 32) {
       float ms, ls;
       load_ml(wr, i + lane, ms, ls);
@@ -1310,9 +1333,11 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
-    M = fmaxf(M, pmax);
-    float l = pm != neg_inf() ? ex2(pm - M) * pl : 0.f;
-    if (pm2 != neg_inf()) l += ex2(pm2 - M) * pl2;
+    const float M = pmax;
+    const float w1 = pm != neg_inf() ? ex2(pm - M) : 0.f, w2 = pm2 != neg_inf() ? ex2(pm2 - M) : 0.f;
+    wts[wr][lane] = w1;
+    wts[wr][lane + 32] = w2;
+    float l = w1 * pl + w2 * pl2;
     for (int i = 64; i < np; i += 32) {
       float ms, ls;
       load_ml(wr, i + lane, ms, ls);
@@ -1334,21 +1359,25 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
   for (int k = 0; k < RPT; ++k) {
     const int rl = rl0 + 8 * k;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k + 1 < RPT) fetch(next, rl + 8, 0);  // the next row's, while this one's are added
-    if (rl < rows) {
-      const int nseg = cnt[rl][0] + cnt[rl][1];
-      const float M = rowM[rl];
-      for (int i0 = 0; i0 < nseg; i0 += NB * SG) {
-        if (i0 > 0) fetch(now, rl, i0);
+    const Row row = here;
+    if (k + 1 < RPT) {
+      here = row_at(rl + 8, c);
+      fetch(next, here, 0);  // the next row's, while this one's are added
+    }
+    auto add = [&](float w, const float4& v) {
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    };
+    for (int i0 = 0; i0 < min(row.n, NW); i0 += NB * SG) {
+      if (i0 > 0) fetch(now, row, i0);
 #pragma unroll
-        for (int q = 0; q < NB; ++q) {
-          const float w = now.ml[q] != neg_inf() ? ex2(now.ml[q] - M) : 0.f;
-          acc.x += w * now.v[q].x;
-          acc.y += w * now.v[q].y;
-          acc.z += w * now.v[q].z;
-          acc.w += w * now.v[q].w;
-        }
-      }
+      for (int q = 0; q < NB; ++q) add(wts[rl][i0 + sg + q * SG], now.v[q]);
+    }
+    for (int i = NW + sg; i < row.n; i += SG) {  // (a row of very many partials)
+      const float m = ml_at(rl, i, row.nS)->x;
+      add(m != neg_inf() ? ex2(m - rowM[rl]) : 0.f, *o_at(row, i));
     }
     if constexpr (SG > 1) {
       part_sum[sg][rl][c] = acc;
