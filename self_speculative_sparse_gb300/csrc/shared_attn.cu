@@ -40,16 +40,14 @@ constexpr int kMaxSlots = 12;  // ring slots (K or V tiles) at most
 // Everything the kernels need about lengths and groups, in the workspace: built from the
 // device arrays by one CTA of a first small kernel, copied to shared memory by the others (built
 // by every CTA for itself it takes each kernel 4 us more).  An item is one unit of rows (a pair
-// of row tiles of a KV head, or one row tile of two KV heads) and its whole key range; it counts
-// one step more than its key tiles, since filling and draining its pipeline costs a CTA about as
-// much as a tile.
-//
-// The attention CTAs split the items' steps evenly.  If any group has pairs of row tiles, the
-// shared items are bound by the tensor cores and the private ones by reading keys and values
-// that one sequence's few rows use once: then the two kinds are split separately, every CTA
-// takes its part of both, and half of them take the private part first (64 sequences x 16384
-// shared and 100 to 1000 private tokens: 152 us, with one split 197).  Without pairs all items
-// are alike, and one split saves a run a CTA (16 sequences x 32768: 41 us, with two 45).
+// of row tiles of a KV head, or one row tile of two KV heads) and its whole key range.  Its steps are
+// its key tiles and kItemSteps more, before them, for what filling a run's pipeline and writing its
+// partials costs a CTA; the attention CTAs split the steps of all items evenly, the shared ones
+// first.  (Attention kernel with 1, 2, 3 and 4 such steps: 131, 117, 110 and 115 us for 64 sequences
+// of 16384 shared and 100 to 1000 private tokens, 55, 57, 57 and 58 for eight of 20011 in three groups,
+// 38 for 16 of 32768 with each.)
+constexpr int kItemSteps = kSharedItemSteps;
+
 struct Meta {
   int* gs;     // [ng + 1] first sequence of a group
   int* eff;    // [ng + 1] tokens of a group read once (a multiple of 128)
@@ -60,7 +58,6 @@ struct Meta {
   int* grp;    // [B] group of a sequence
   int* stepP;  // [B + 1] attention steps of private ranges before a sequence
   int* scP;    // [B + 1] score items of private ranges before a sequence
-  int* two;    // [1] whether the private items are split by themselves
 };
 
 // What the combine kernel needs of a sequence, in one load; the record after the last sequence's
@@ -69,10 +66,10 @@ struct __align__(16) SeqRec {
   int n, eff;         // checked length; tokens read once for its group
   int row0, pairs;    // its first query row among the group's; row-tile pairs of the group
   int stepS, itemS;   // shared steps and items before its group
-  int stepP, two;     // private steps before it; Meta::two
+  int stepP, pad;     // private steps before it
 };
 
-__host__ __device__ inline int meta_ints(int B, int ng) { return 5 * (ng + 1) + 2 * B + 2 * (B + 1) + 1; }
+__host__ __device__ inline int meta_ints(int B, int ng) { return 5 * (ng + 1) + 2 * B + 2 * (B + 1); }
 
 __device__ __forceinline__ Meta meta_at(int* base, int B, int ng) {
   Meta m;
@@ -85,7 +82,6 @@ __device__ __forceinline__ Meta meta_at(int* base, int B, int ng) {
   m.grp = m.nlen + B;
   m.stepP = m.grp + B;
   m.scP = m.stepP + B + 1;
-  m.two = m.scP + B + 1;
   return m;
 }
 
@@ -184,7 +180,6 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
   }
   __syncthreads();
   int steps[PER], items[PER], sc[PER], eff[PER], sum[3] = {0, 0, 0};
-  bool pair = false;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     const int g = tid * PER + k;
@@ -203,16 +198,14 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
       row_tiles(members, p, pairs, odd);
       const int tiles = eff[k] / KT;
       items[k] = tiles ? p.Hkv * pairs + odd * Hp : 0;
-      steps[k] = items[k] * (tiles + 1);
+      steps[k] = items[k] * (tiles + kItemSteps);
       sc[k] = tiles * ((members + p.nsc - 1) / p.nsc);
-      pair |= tiles > 0 && pairs > 0;
     }
     sum[0] += steps[k];
     sum[1] += items[k];
     sum[2] += sc[k];
   }
   int at[3], tot[3];
-  pair = __syncthreads_or(pair);
   cta_scan<3, WARPS>(sum, at, tot, sh);
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -232,7 +225,6 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
     m.stepS[ng] = tot[0];
     m.itemS[ng] = tot[1];
     m.scS[ng] = tot[2];
-    *m.two = pair;
   }
   __syncthreads();
   int tiles[PER], sum2[2] = {0, 0};
@@ -240,7 +232,7 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
   for (int k = 0; k < PER; ++k) {
     const int b = tid * PER + k;
     tiles[k] = b < B && m.nlen[b] >= 0 ? (m.nlen[b] - m.eff[m.grp[b]] + KT - 1) / KT : 0;
-    sum2[0] += tiles[k] > 0 ? (tiles[k] + 1) * Hp : 0;
+    sum2[0] += tiles[k] > 0 ? (tiles[k] + kItemSteps) * Hp : 0;
     sum2[1] += tiles[k];
   }
   int at2[2], tot2[2];
@@ -252,7 +244,7 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
       m.stepP[b] = at2[0];
       m.scP[b] = at2[1];
     }
-    at2[0] += tiles[k] > 0 ? (tiles[k] + 1) * Hp : 0;
+    at2[0] += tiles[k] > 0 ? (tiles[k] + kItemSteps) * Hp : 0;
     at2[1] += tiles[k];
   }
   if (tid == 0) {
@@ -266,7 +258,7 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
 // The first kernel of a call.  CTA 0: the layout.  The others (with scores), one a sequence: the sum
 // of its masked query rows of each KV head, in fp32, as three bf16 parts whose sum is it to 2^-24.
 __global__ void __launch_bounds__(1024) shared_prep_kernel(const SharedParams p) {
-  __shared__ int space[5 * (kMaxBatch + 1) + 2 * kMaxBatch + 2 * (kMaxBatch + 1) + 1], sh[3][32];
+  __shared__ int space[5 * (kMaxBatch + 1) + 2 * kMaxBatch + 2 * (kMaxBatch + 1)], sh[3][32];
   pdl_launch_dependents();
   pdl_wait();
   if (blockIdx.x > 0) {
@@ -297,7 +289,7 @@ __global__ void __launch_bounds__(1024) shared_prep_kernel(const SharedParams p)
   SeqRec* rec = reinterpret_cast<SeqRec*>(p.rec);
   for (int b = threadIdx.x; b <= p.B; b += 1024) {
     if (b == p.B) {
-      rec[b] = SeqRec{0, 0, 0, 0, m.stepS[p.n_groups], m.itemS[p.n_groups], m.stepP[p.B], *m.two};
+      rec[b] = SeqRec{0, 0, 0, 0, m.stepS[p.n_groups], m.itemS[p.n_groups], m.stepP[p.B], 0};
     } else {
       const int g = m.grp[b];
       int pairs, odd;
@@ -331,46 +323,17 @@ struct __align__(16) RunRec {
 };
 static_assert(sizeof(RunRec) == 64, "");
 
-// The split of the shared (part 0) or private steps: T steps over nc CTAs, as many as have one;
-// the part's step x is step x + first of them.
-struct Split {
-  int T, nc, first;
-};
-__device__ __forceinline__ Split split_of(int part, int totS, int totP, bool two, int nctas) {
-  const int T = two ? (part ? totP : totS) : totS + totP;
-  return Split{T, min(T, nctas), part && !two ? totS : 0};
-}
-
-// The steps of a part that this CTA owns, from the value returned up to x1; cta: its index in the
-// part's split.  (A private split of its own runs from the other end of the grid, so that the few
-// steps of a small one fall to other CTAs than the first shared ones.)
-__device__ __forceinline__ int my_steps(const SharedParams& p, const Meta& m, int part, int& x1, int& cta) {
-  const int totS = m.stepS[p.n_groups], totP = m.stepP[p.B];
-  const bool two = *m.two != 0;
-  const Split s = split_of(part, totS, totP, two, p.nctas);
-  const int tot = part ? totP : totS;
-  cta = part && two ? p.nctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
-  x1 = 0;
-  if (cta >= s.nc) return 0;
-  x1 = min(static_cast<int>(split_begin(cta + 1, s.T, s.nc)) - s.first, tot);
-  return min(max(static_cast<int>(split_begin(cta, s.T, s.nc)) - s.first, 0), tot);
-}
-// A CTA's parts in the order it works on them.
-__device__ __forceinline__ int part_of(const Meta& m, int pass) {
-  return pass ^ (*m.two ? static_cast<int>(blockIdx.x & 1) : 0);
-}
-
-// The run at step x of a part, of a CTA that ends at xend; x moves past it (ntiles may be 0).
-__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int part, int& x, int xend) {
+// The run at step x of a CTA that ends at xend; x moves past it (ntiles may be 0 or less).
+__device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, int& x, int xend) {
   Run r;
-  const int Hp = (p.Hkv + 1) / 2;
+  const int Hp = (p.Hkv + 1) / 2, totS = m.stepS[p.n_groups];
   int off, len;  // step within the item, the item's steps
-  if (part == 0) {
+  if (x < totS) {
     const int g = find(m.stepS, p.n_groups, x);
     const int members = m.gs[g + 1] - m.gs[g];
     int pairs, odd;
     row_tiles(members, p, pairs, odd);
-    len = m.eff[g] / KT + 1;
+    len = m.eff[g] / KT + kItemSteps;
     off = x - m.stepS[g];
     const int it = off / len;
     off -= it * len;
@@ -394,10 +357,10 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
       r.r0[0] = r.r0[1] = pairs * 2 * p.RT;
     }
   } else {
-    const int b = find(m.stepP, p.B, x);
+    const int b = find(m.stepP, p.B, x - totS);
     const int eff = m.eff[m.grp[b]];
-    len = (m.nlen[b] - eff + KT - 1) / KT + 1;
-    off = x - m.stepP[b];
+    len = (m.nlen[b] - eff + KT - 1) / KT + kItemSteps;
+    off = x - totS - m.stepP[b];
     const int hp = off / len;
     off -= hp * len;
     r.row = b;
@@ -411,9 +374,9 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     r.head[1] = 2 * hp + 1;
     r.r0[0] = r.r0[1] = 0;
   }
-  const int take = min(len - off, xend - x);  // the item's first step has no tile
-  r.tile0 = off > 0 ? off - 1 : 0;
-  r.ntiles = off + take - 1 - r.tile0;
+  const int take = min(len - off, xend - x);  // (the item's first steps have no tile)
+  r.tile0 = max(off - kItemSteps, 0);
+  r.ntiles = off + take - kItemSteps - r.tile0;
   x += take;
   return r;
 }
@@ -716,21 +679,20 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     // leaves them in shared memory (each of the 20 warps for itself took 3000 cycles a run, most
     // of it for instructions out of cache).
     const Meta m = meta_at(mbase, p.B, p.n_groups);
-    int pass = -1, x = 0, x1 = 0, cta = 0, planned = 0;
+    const int T = m.stepS[p.n_groups] + m.stepP[p.B], nc = min(T, p.nctas), cta = blockIdx.x;
+    int x = cta < nc ? static_cast<int>(split_begin(cta, T, nc)) : 0, planned = 0;
+    const int x1 = cta < nc ? static_cast<int>(split_begin(cta + 1, T, nc)) : 0;
+    bool ended = false;
     auto plan = [&] {
-      if (pass == 2) return true;
+      if (ended) return true;
       RunRec out{kPair, -1, 0, 0, 0, 0, 0, 0, {0, 0}, {0, 0}, 0, {0, 0, 0}};
-      while (out.ntiles <= 0) {
-        if (x >= x1) {
-          if (++pass == 2) break;
-          x = my_steps(p, m, part_of(m, pass), x1, cta);
-          continue;
-        }
-        const Run r = make_run(p, m, part_of(m, pass), x, x1);
+      while (x < x1 && out.ntiles <= 0) {
+        const Run r = make_run(p, m, x, x1);
         out = RunRec{r.mode, r.ntiles, r.tile0, r.ntok, r.tok0, r.row, r.rows, r.priv, {r.head[0], r.head[1]},
                      {r.r0[0], r.r0[1]}, (cta + r.item) * 2, {0, 0, 0}};
       }
-      if (pass == 2) out.ntiles = -1;
+      ended = out.ntiles <= 0;
+      if (ended) out.ntiles = -1;
       if (planned >= kRuns &&
           !warp_wait(&run_empty[planned % kRuns], (planned / kRuns - 1) & 1, p.status, abort))
         return false;
@@ -1177,23 +1139,22 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
     const SeqRec tot = reinterpret_cast<const SeqRec*>(p.rec)[p.B];
     const int r = r0 + tid, tiles = rec.eff / KT, ptiles = (n - rec.eff + KT - 1) / KT;
     cnt[tid][0] = cnt[tid][1] = 0;
+    const int T = tot.stepS + tot.stepP, nc = min(T, p.nctas);
     if (tiles > 0) {
-      const Split sp = split_of(0, tot.stepS, tot.stepP, tot.two, p.nctas);
       const int rr = rec.row0 + r, rt = rr / p.RT;
       const bool pair = (rt >> 1) < rec.pairs;
       const int it = pair ? g * rec.pairs + (rt >> 1) : p.Hkv * rec.pairs + (g >> 1);
-      const int s0 = rec.stepS + it * (tiles + 1) + sp.first;
-      const int cs = static_cast<int>(owner_cta(s0 + 1, sp.T, sp.nc));
-      cnt[tid][0] = static_cast<int>(owner_cta(s0 + tiles, sp.T, sp.nc)) - cs + 1;
+      const int s0 = rec.stepS + it * (tiles + kItemSteps) + kItemSteps;  // its first tile
+      const int cs = static_cast<int>(owner_cta(s0, T, nc));
+      cnt[tid][0] = static_cast<int>(owner_cta(s0 + tiles - 1, T, nc)) - cs + 1;
       const uint32_t u = (cs + rec.itemS + it) * 2 + (pair ? rt & 1 : g & 1);
       at[tid][0] = u * (KT * D / 4) + (rr - rt * p.RT);
       at[tid][1] = u * KT + (rr - rt * p.RT);
     }
     if (ptiles > 0) {
-      const Split sp = split_of(1, tot.stepS, tot.stepP, tot.two, p.nctas);
-      const int s0 = rec.stepP + (g >> 1) * (ptiles + 1) + sp.first;
-      const int cp = static_cast<int>(owner_cta(s0 + 1, sp.T, sp.nc));
-      cnt[tid][1] = static_cast<int>(owner_cta(s0 + ptiles, sp.T, sp.nc)) - cp + 1;
+      const int s0 = tot.stepS + rec.stepP + (g >> 1) * (ptiles + kItemSteps) + kItemSteps;
+      const int cp = static_cast<int>(owner_cta(s0, T, nc));
+      cnt[tid][1] = static_cast<int>(owner_cta(s0 + ptiles - 1, T, nc)) - cp + 1;
       const uint32_t u = (cp + b * ((p.Hkv + 1) / 2) + (g >> 1)) * 2 + (g & 1);
       at[tid][2] = u * (p.Mpad * (D / 4)) + r;
       at[tid][3] = u * p.Mpad + r;

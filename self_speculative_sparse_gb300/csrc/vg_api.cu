@@ -1298,7 +1298,7 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   DevInfo di;
   if ((st = device_info(&di)) != VG_OK) return st;
   const SharedWs w = shared_ws(s, groups->n_groups, di.sms);
-  if (w.items * (s.max_len / kSharedTileKeys + 2) > 0x7fffffffLL)
+  if (w.items * (s.max_len / kSharedTileKeys + kSharedItemSteps + 1) > 0x7fffffffLL)
     return fail(VG_ERR_UNSUPPORTED_SHAPE, "B=%d sequences of up to max_len=%d tokens are too many tiles", s.B, s.max_len);
   if (!ws) return fail(VG_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", w.total);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(VG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
@@ -1313,7 +1313,10 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
   if ((st = encode_cache_map(&tmV, cache->V, cache->capacity_slots, s.Hkv, s.D, verify_box_rows(cache))) != VG_OK) return st;
   if ((st = encode_map_3d(&tmQ, q, s.D, s.Hq, static_cast<int64_t>(s.B) * s.R, s.G, kSharedTileKeys / s.G)) != VG_OK)
     return st;
-  p.nsc = s.B <= 16 ? 16 : 32;  // (64 leave room for two stages only: 33 us instead of 26 with 64 sequences)
+  // Members of one score item.  Fewer bring fewer query parts with each key tile, more read a key tile
+  // of many members fewer times (the score kernel with 16 and 32: 30 and 31 us for 8 sequences, 33 and
+  // 29 for 64; 64 members leave room for two stages only and take 33).
+  p.nsc = s.B <= 16 ? 16 : 32;
   tmZ = tmZ1 = tmK;
   if (row_mask) {
     if ((st = encode_map_3d(&tmZ, p.qsum, s.Hkv * s.D, p.Bpad, 3, p.nsc, 3)) != VG_OK) return st;

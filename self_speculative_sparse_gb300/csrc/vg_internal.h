@@ -116,6 +116,8 @@ struct AcceptParams {
 
 // Keys of a tile of the shared-prefix kernels, and the rows of one lane's tile.
 constexpr int kSharedTileKeys = 128;
+// Steps that an item of the attention kernel counts beside its key tiles.
+constexpr int kSharedItemSteps = 3;
 
 struct SharedParams {
   const __nv_bfloat16* q;      // [B][R][Hq][D]
