@@ -19,10 +19,19 @@
 //   heads  the lanes are the same row tile of two KV heads, each with its own K and V tile
 //          (a group's odd last row tile, and every private range).
 // While one lane's warps run the softmax of their tile, the tensor cores work for the other
-// (P V of its tile, then Q K^T of its next).  P goes back to tensor memory as bf16, over the
-// columns of S, and is the A operand of P V from there: it never passes shared memory.
+// (P V of its tile, then Q K^T of its next): the lanes' issuers take turns.  P goes back to tensor
+// memory as bf16, over the columns of S, and is the A operand of P V from there: it never passes
+// shared memory.
 // Warps: 0-7 and 8-15 the lanes (two threads a row), 16 and 18 the TMA producers, 17 and 19
-// the lanes' MMA issuers.
+// the lanes' MMA issuers; 16 also plans the CTA's runs.
+//
+// What bounds it: 2048 cycles of tensor-core work a step of two lanes with d = 128, or 128 KB of
+// keys and values a step in heads mode.  In the middle of a run a pair step takes 2700 cycles,
+// about the rate at which a plain bf16 product runs on this card; a run's start and end (the first
+// tile's latency, the first maximum, partials of 64 KB a lane) cost it another 8000.  64 sequences of
+// 8 rows and 32 heads over 16384 shared and 100 to 1000 private tokens take it 111 us (140 GFLOP:
+// 1.26 PFLOP/s, 66% of a plain product's rate); 16 of one row over 32768 tokens 37 us
+// (134 MB of shared keys and values: 3.6 TB/s; the first tile is there after 18000 of 67000 cycles).
 #include "vg_common.cuh"
 #include "vg_internal.h"
 
@@ -38,12 +47,12 @@ constexpr int kMaxSlots = 12;  // ring slots (K or V tiles) at most
 
 // ---------------------------------------------------------------- the batch's layout
 // Everything the kernels need about lengths and groups, in the workspace: built from the
-// device arrays by one CTA of a first small kernel, copied to shared memory by the others (built
-// by every CTA for itself it takes each kernel 4 us more).  An item is one unit of rows (a pair
-// of row tiles of a KV head, or one row tile of two KV heads) and its whole key range.  Its steps are
-// its key tiles and kItemSteps more, before them, for what filling a run's pipeline and writing its
-// partials costs a CTA; the attention CTAs split the steps of all items evenly, the shared ones
-// first.  (Attention kernel with 1, 2, 3 and 4 such steps: 131, 117, 110 and 115 us for 64 sequences
+// device arrays by one CTA of a first small kernel, copied to shared memory by the others (built by
+// every attention CTA for itself, in place of that kernel, it takes the CTAs 6 us).  An item is one unit
+// of rows (a pair of row tiles of a KV head, or one row tile of two KV heads) and its whole key range.
+// Its steps are its key tiles and, before them, kItemSteps more for what filling a run's pipeline and
+// writing its partials costs a CTA; the attention CTAs split the steps of all items evenly, the shared
+// ones first.  (Attention kernel with 1, 2, 3 and 4 such steps: 131, 117, 110 and 115 us for 64 sequences
 // of 16384 shared and 100 to 1000 private tokens, 55, 57, 57 and 58 for eight of 20011 in three groups,
 // 38 for 16 of 32768 with each.)
 constexpr int kItemSteps = kSharedItemSteps;
@@ -1386,6 +1395,11 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
 // parts and the heads' tiles in fp32 registers (the tensor core's own sum runs over one part of
 // one head) and write rows of consecutive positions.  A private range has one member: its
 // items bring and multiply the 16 columns an MMA has at least.
+//
+// What bounds it: the keys' bytes, once its ring is full: 8 sequences over three prompts of 20011 tokens
+// and 8 KV heads take 29.5 us for 123 MB of shared keys, a stage of 32 KB every 1200 cycles (7.8 TB/s,
+// partly out of L2) after a start of 7000.  64 members over one prompt bring 24 KB of query parts with
+// each 32 KB of keys, and three stages do not cover the latency: 29 us for 105 MB.
 template <int D, int N>
 struct ZCfg {
   static constexpr int HALVES = D / 64;
