@@ -358,6 +358,8 @@ vg_status vg_accept(int32_t B, int32_t gamma, int32_t V, const float* p_logits, 
  *   row_mask, scores     as row_mask0, scores0 of vg_verify_attn: scores for every prefix entry
  *                        of every sequence, shared ones included; both 0 / NULL to leave out
  *   others               as vg_verify_attn (page_size 8, 16, 32 or a multiple of 64)
+ * With d = 128, 5 * n_groups + 4 * B beyond about 8500 is refused (VG_ERR_UNSUPPORTED_SHAPE): the
+ * batch's layout has to fit beside the tiles in shared memory.
  * A group_start that is not such a list, or a shared_len out of range, is reported as
  * VG_ERR_DEVICE_BOUNDS, and the group's (or every) sequence is then read by itself.
  * Workspace: at least vg_shared_verify_workspace_size(dims, groups) bytes (only n_groups is
@@ -504,7 +506,8 @@ vg_status vg_pages_fork(const vg_page_pool* pool, const vg_kv_cache* caches, int
  * ones below it (ascending into ascending), contents of every layer included; afterwards
  * pages 0 .. n_live - 1 are in use.  Entries of the rows that held a moved page name its new
  * place in page_table_out, and its references are in refs_out; both may be the pool's own
- * arrays (in place) or must not overlap them.  Entries past held are copied as they are.
+ * arrays (in place) or must not overlap them.  Entries past held are copied as they are.  A
+ * page kept from use by a reference of its own moves like any other: keep such pages at the front.
  * Moved pages' old contents stay where they were.  n_live: device int32 (the count).
  */
 vg_status vg_pages_compact(const vg_page_pool* pool, const vg_kv_cache* caches, int32_t n_layers, int32_t token_bytes,

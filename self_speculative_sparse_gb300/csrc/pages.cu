@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
 constexpr int kSmallRequests = 1024;
 constexpr int kSmallPages = kPageMaxCluster * kPageThreads * 32;
 constexpr int kHash = 2048;
+static_assert(kSmallRequests <= kPageThreads && 2 * kSmallRequests <= kHash && kHash == 1 << (32 - 21), "see slot_of");
 
 __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const PagesParams p) {
   cg::cluster_group cluster = cg::this_cluster();

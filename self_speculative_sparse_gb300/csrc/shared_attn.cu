@@ -944,7 +944,10 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       const RunRec* rec = recs;
       int mode = kPair, last = 0, keys = KT, nrows = KT;
       if (real) {
-        if (!(rec = run_at(k))) break;
+        rec = run_at(k);
+        // (the two warps of a pair meet at named barriers, which have no limit: after a lost wait they
+        // leave together)
+        if (named_bar_or(pair_bar, 64, rec == nullptr)) break;
         mode = rec->mode;
         last = rec->ntiles - 1;
         keys = rec->ntok - rec->tile0 * KT;

@@ -130,6 +130,9 @@ class LayerState:
         """Rotate the verify rows' q ([B * (gamma + 1)][H_q][d], in place without q_out) and k, and
         append k and v behind the prefixes (then ``verify(append=False)``)."""
         q_out = q if q_out is None else q_out
+        for t in (q, k, v, q_out):  # (only the rows may be apart)
+            if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != t.shape[2]):
+                raise ValueError("q, k, v and q_out: each row's heads must lie together")
         vb.vg_rope_append(self.dims, self.cache, rope, q, q.stride(0), k, k.stride(0), v, v.stride(0), None,
                           q.shape[0], self.prefix_len, q_out, q_out.stride(0), dev_status=self.status, stream=stream)
 

@@ -320,6 +320,18 @@ def test_many_sequences_and_many_runs_of_a_cta(scores):
     c.check(K0=K0, V0=V0)
 
 
+def test_as_many_groups_as_sequences():
+    def case(d):
+        return Case([1] * 1024, [130] * 1024, [[i % 3] for i in range(1024)], Hq=2, Hkv=1, d=d, page=16)
+    c = case(64)
+    K0, V0 = c.K.clone(), c.V.clone()
+    c.call()
+    c.check(K0=K0, V0=V0)
+    with pytest.raises(vb.VgError) as e:  # the layout does not fit beside four tiles of 128 columns
+        case(128).call()
+    assert e.value.status == vb.VG_ERR_UNSUPPORTED_SHAPE
+
+
 def test_two_captured_calls_share_a_workspace():
     a = Case([4, 2], [600, 260], [[0, 10, 200, 300], [5, 600]], gamma=2, append=False, seed=1)
     b = Case([7], [1000], [[i * 31 for i in range(7)]], gamma=1, append=False, seed=2, scores=False, d=64)
