@@ -225,3 +225,48 @@ def test_branches_of_a_prompt(prompt):
             run.tokens[layer][5] = [t.clone() for t in run.tokens[layer][2]]
         assert pool.n_live.item() == sum(r > 0 for r in sim.refs)
         run.cache_holds_the_tokens(lens)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_a_layers_state_rotates_appends_and_verifies(page):
+    import synth
+    from self_speculative_sparse_gb300.runtime import LayerState
+    w = synth.Workload("branches", B=5, Hq=HQ, Hkv=HKV, d=D, gamma=GAMMA, k=64, n=300)
+    data = w.layer_pool(0)
+    shared = 261
+    o = data["seq_offset"]
+    for b in range(1, w.B):
+        for x in (data["K"], data["V"]):
+            x[o[b]:o[b] + shared] = x[o[0]:o[0] + shared]
+    if page:
+        data = synth.to_paged(w, data, page)
+    st = LayerState(w, data)
+    rows = w.B * w.R
+    inv = oracle.rope_inverse(D, 10000.0)
+    freq = torch.from_numpy(vb.vg_rope_freqs(D, 10000.0).view(np.int64)).cuda()
+    q0, k0 = st.q_verify.clone(), st.k_new.clone()
+    with pytest.raises(ValueError):
+        st.rope_append(vb.make_rope(freq, D), st.q_verify.reshape(rows, HQ, D)[..., ::2], st.k_new, st.v_new)
+    st.rope_append(vb.make_rope(freq, D), st.q_verify.view(rows, HQ, D), st.k_new.view(rows, HKV, D),
+                   st.v_new.view(rows, HKV, D))
+    groups = vb.make_groups(None, ints([shared]))
+    ws = torch.empty(vb.vg_shared_verify_workspace_size(st.dims, groups), dtype=torch.uint8, device="cuda")
+    st.verify_shared(groups, ws, append=False)
+    torch.cuda.synchronize()
+    assert st.check_status() == 0
+    K, V = bf16_to_f64(st.K), bf16_to_f64(st.V)
+    q, out, sc = bf16_to_f64(st.q_verify), bf16_to_f64(st.out_verify), st.scores0.cpu().numpy()
+    for b in range(w.B):
+        n = int(data["prefix_len"][b])
+        at = (oracle.paged_slots(data["page_table"][b], page, n + w.R) if page else o[b] + np.arange(n + w.R))
+        pos = n + np.arange(w.R)
+        for x0, x in ((bf16_to_f64(q0[b]), q[b]), (bf16_to_f64(k0[b]), K[at[n:]])):
+            want = oracle.rope(x0, pos, inv, False)
+            pair = np.hypot(x0[..., :D // 2], x0[..., D // 2:])
+            assert (np.abs(x - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * np.concatenate([pair, pair], -1)).all()
+        assert np.array_equal(V[at[n:]], bf16_to_f64(st.v_new[b]))
+        attention_close(out[b], q[b], K[at[:n]], V[at[:n]], K[at[n:]], V[at[n:]])
+        want = oracle.aggregated_scores(q[b], K[at[:n]], w.rows("c2"))
+        size = np.einsum("hd,nhd->n", np.abs(q[b][w.rows("c2")]).reshape(-1, HKV, HQ // HKV, D).sum((0, 2)),
+                         np.abs(K[at[:n]])) / np.sqrt(D)
+        assert (np.abs(sc[b, :n] - want) <= 2.0 ** -18 * size).all()
