@@ -152,6 +152,8 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
   constexpr int NT = WARPS * 32, PER = (kMaxBatch + NT - 1) / NT;
   const int tid = threadIdx.x, B = p.B, ng = p.n_groups, Hp = (p.Hkv + 1) / 2;
   bool good = true;
+  // (asked for together with the lengths)
+  const int start0 = p.group_start && tid <= ng ? p.group_start[tid] : 0, shared0 = tid < ng ? p.shared_len[tid] : 0;
   for (int b = tid; b < B; b += NT) {
     int n = p.prefix_len[b];
     bool ok = n >= 0 && n <= p.max_len;
@@ -170,9 +172,9 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
   int* least = m.stepS;   // (until the scan) the shortest member
   int* shared = m.itemS;  // (until the scan) the shared length asked for
   for (int g = tid; g <= ng; g += NT) {
-    m.gs[g] = p.group_start ? p.group_start[g] : (g ? B : 0);
+    m.gs[g] = !p.group_start ? (g ? B : 0) : g == tid ? start0 : p.group_start[g];
     if (g < ng) {
-      shared[g] = p.shared_len[g];
+      shared[g] = g == tid ? shared0 : p.shared_len[g];
       least[g] = 0x7fffffff;
     }
   }
@@ -268,14 +270,17 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
 
 // The first kernel of a call.  CTA 0: the layout.  The others (with scores), one a sequence: the sum
 // of its masked query rows of each KV head, in fp32, as three bf16 parts whose sum is it to 2^-24.
-__global__ void __launch_bounds__(1024) shared_prep_kernel(const SharedParams p) {
+// 512 threads: 6.0 to 6.7 us with 16 sequences by itself, most of it the launch and a dozen dependent
+// steps (1024 threads take 0.7 us more, 128 with scores 3 us more).
+constexpr int kPrepThreads = 512;
+__global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const SharedParams p) {
   __shared__ int space[5 * (kMaxBatch + 1) + 2 * kMaxBatch + 2 * (kMaxBatch + 1)], sh[3][32];
   pdl_launch_dependents();
   pdl_wait();
   if (blockIdx.x > 0) {
     const int b = blockIdx.x - 1, width = p.Hkv * p.D;
     const size_t part = static_cast<size_t>(p.Bpad) * width;
-    for (int e = threadIdx.x; e < width; e += 1024) {
+    for (int e = threadIdx.x; e < width; e += kPrepThreads) {
       const int g = e / p.D, d = e - g * p.D;
       float acc = 0.f;
       for (uint32_t bits = p.mask; bits != 0u; bits &= bits - 1u) {
@@ -295,10 +300,10 @@ __global__ void __launch_bounds__(1024) shared_prep_kernel(const SharedParams p)
     return;
   }
   const Meta m = meta_at(space, p.B, p.n_groups);
-  if (!build_layout<32>(p, m, sh)) report(p.status, VG_ERR_DEVICE_BOUNDS);
-  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += 1024) p.meta[i] = space[i];
+  if (!build_layout<kPrepThreads / 32>(p, m, sh)) report(p.status, VG_ERR_DEVICE_BOUNDS);
+  for (int i = threadIdx.x; i < meta_ints(p.B, p.n_groups); i += kPrepThreads) p.meta[i] = space[i];
   SeqRec* rec = reinterpret_cast<SeqRec*>(p.rec);
-  for (int b = threadIdx.x; b <= p.B; b += 1024) {
+  for (int b = threadIdx.x; b <= p.B; b += kPrepThreads) {
     if (b == p.B) {
       rec[b] = SeqRec{0, 0, 0, 0, m.stepS[p.n_groups], m.itemS[p.n_groups], m.stepP[p.B], 0};
     } else {
@@ -1635,7 +1640,7 @@ cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const
                             const CUtensorMap& tmQ, const CUtensorMap& tmZ, const CUtensorMap& tmZ1,
                             cudaStream_t stream) {
   cudaError_t e;
-  Launch f(p.mask ? 1 + p.B : 1, 1024, 0, stream);
+  Launch f(p.mask ? 1 + p.B : 1, kPrepThreads, 0, stream);
   if ((e = cudaLaunchKernelEx(&f.cfg, shared_prep_kernel, p)) != cudaSuccess) return e;
   if (p.mask) {
     e = p.nsc == 16 ? launch_scores<D, 16>(p, tmK, tmZ, tmZ1, stream) : launch_scores<D, 32>(p, tmK, tmZ, tmZ1, stream);
