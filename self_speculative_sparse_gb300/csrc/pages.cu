@@ -89,6 +89,19 @@ struct ClusterShared {
   int counts[kPageMaxCluster];  // every CTA's count, pushed by its owner
 };
 
+// Cluster barriers, where a cluster of one CTA needs no more than its own (a request for
+// 16 rows: 5.2 us, with the cluster's 6.2).
+__device__ __forceinline__ void cluster_arrive(int C) {
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait(int C) {
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync(int C) {
+  if (C > 1) cg::this_cluster().sync();
+  else __syncthreads();
+}
+
 // Grow, cut or fork rows (one cluster).
 __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const PagesParams p) {
   cg::cluster_group cluster = cg::this_cluster();
@@ -107,12 +120,12 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
       if (f >= 0 && f < p.n_seqs) p.owner[f] = INT_MAX;
     }
   }
-  cluster.sync();
+  cluster_sync(C);
   for (int j = gt; j < p.n; j += GT) {
     const int c = p.seq ? p.seq[j] : j;
     if (c >= 0 && c < p.n_seqs) atomicMin(p.owner + c, j);
   }
-  cluster.sync();
+  cluster_sync(C);
   // ---- check each request, give back what its row no longer holds
   for (int j = gw; j < p.n; j += GW) {
     const int c = p.seq ? p.seq[j] : j;
@@ -155,7 +168,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
       p.have[j] = ok ? have : -1;
     }
   }
-  cluster.sync();
+  cluster_sync(C);
   // ---- free pages of every CTA's share; each request's rank among the pages handed out
   int lo, hi, mine, run_free;
   page_run(p.n_pages, rank, C, lo, hi);
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
     }
     if (tid == 0) *p.needed = all;
   }
-  cluster.sync();
+  cluster_sync(C);
   // ---- the lowest free pages, as many as are asked for
   int base = before, free_all = 0;
   for (int c = 0; c < C; ++c) {
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
     for (int i = lo; i < hi && base < needed; ++i)
       if (__ldcg(p.refs + i) <= 0) p.freelist[base++] = i;
   }
-  cluster.sync();
+  cluster_sync(C);
   pdl_launch_dependents();
   // ---- fill the rows
   for (int j = gw; j < p.n; j += GW) {
@@ -230,8 +243,9 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_kernel(const Pages
 // finds the first request that names a row; (2) a warp a request gives back the pages that its
 // row no longer holds; (3) every CTA counts the free pages of its share of the pool, kept as a
 // mask in registers; (4) the thread of a free page finds the request whose page it becomes by
-// its rank, and writes it there.  A request for 16 rows of a pool of 1024 pages takes 6.2 us so
-// and 11 us with the kernel above; for 512 rows of 131072 pages 8 to 12 us and 16 to 17.
+// its rank, and writes it there.  A request for 16 rows of a pool of 1024 pages takes 5.2 us so
+// and 11 us with the kernel above; for 512 rows of 131072 pages 9 to 12 us and 16 to 17.  (256 threads for
+// a small pool are no faster.)
 constexpr int kSmallRequests = 1024;
 constexpr int kSmallPages = kPageMaxCluster * kPageThreads * 32;
 constexpr int kHash = 2048;
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
     hash_row[i] = -1;
     hash_first[i] = INT_MAX;
   }
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  cluster_arrive(C);
   __syncthreads();
   pdl_wait();
   // ---- check the requests
@@ -317,8 +331,8 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
       }
     }
   }
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory may be written
-  cluster.sync();
+  cluster_wait(C);  // every CTA runs: its shared memory may be written
+  cluster_sync(C);
   // ---- the free pages of every CTA's share (and, while the counts come, the requests' places among
   // the pages handed out)
   int lo, hi, mine, needed, start = 0;
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_request_small_kernel(const
   }
   const int before = block_scan(__popc(mask), s.sh, &mine);
   if (tid < C) *cluster.map_shared_rank(s.counts + rank, tid) = mine;
-  cluster.sync();
+  cluster_sync(C);
   pdl_launch_dependents();
   int base = before, free_all = 0;
   for (int r = 0; r < C; ++r) {
@@ -410,15 +424,15 @@ __global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const Pages
   __shared__ ClusterShared s;
   const int tid = threadIdx.x;
   const int gt = rank * kPageThreads + tid, GT = C * kPageThreads;
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  cluster_arrive(C);
   pdl_wait();
   int lo, hi, mine;
   page_run(p.n_pages, rank, C, lo, hi);
   const int run_free = count_free(p.refs, lo, hi);
   const int before = block_scan(run_free, s.sh, &mine);
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory may be written
+  cluster_wait(C);  // every CTA runs: its shared memory may be written
   if (tid < C) *cluster.map_shared_rank(s.counts + rank, tid) = mine;
-  cluster.sync();
+  cluster_sync(C);
   int free_before = before, free_all = 0;  // free pages before this run, in all
   for (int c = 0; c < C; ++c) {
     if (c < rank) free_before += s.counts[c];
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const Pages
   }
   if (n_live == p.n_pages && gt == 0) *p.needed = 0;  // (no page at index n_live)
   if (gt == 0) *p.n_live = n_live;
-  cluster.sync();
+  cluster_sync(C);
   const int moves = __ldcg(p.needed);
   pdl_launch_dependents();
   for (int r = gt; r < moves; r += GT) {
