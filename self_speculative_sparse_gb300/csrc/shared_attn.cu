@@ -1123,9 +1123,9 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
 // private ones by CTA, the causal values: a fixed order.
 //
 // What bounds it is instructions, most of them addresses and the short sums: there are some ten
-// products for each of a row's 128 columns (64 sequences x 32 rows x 8 heads: 28.7 us at 0.7
+// products for each of a row's 128 columns (64 sequences x 32 rows x 8 heads: 27 us at 0.7
 // instructions a cycle and partition, whether 4, 5 or 6 CTAs fit an SM; 32 us with 16 rows a CTA, 36
-// with 32.  Without the logits it would take 24 us, without the verify rows' keys and values 25).
+// with 32.  Of its time the logits take about 4 us, the staging of the verify rows' keys and values 4).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParams p) {
   constexpr int PER = D / 32, WARPS = D / 16, CH = D / 8, NT = 2 * D;
@@ -1652,8 +1652,8 @@ cudaError_t launch_shared_t(const SharedParams& p, const CUtensorMap& tmK, const
   Launch a(p.nctas, C::THREADS, smem, stream);
   if ((e = cudaLaunchKernelEx(&a.cfg, shared_attn_kernel<D>, p, tmK, tmV, tmQ)) != cudaSuccess) return e;
   // rows of a CTA share their staging, but fewer CTAs than SMs leave SMs idle (16 sequences of one
-  // row and 4 heads a KV head: 10.5 us with two rows a CTA, 13.7 with eight; 8 sequences of 7
-  // rows: 17.5 and 13.0)
+  // row and 4 heads a KV head: 9.5 us with two rows a CTA, 12.5 with eight; 8 sequences of 7
+  // rows: 14.9 and 10.8; 64 of 8 rows: 91 and 27)
   const int bg = p.B * p.Hkv;
   if (bg * ((p.M + 7) / 8) >= p.nctas) {
     Launch c(bg * ((p.M + 7) / 8), 2 * D, 0, stream);
