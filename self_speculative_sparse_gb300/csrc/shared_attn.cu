@@ -199,14 +199,14 @@ __device__ bool build_layout(const SharedParams& p, const Meta& m, int (*sh)[32]
     steps[k] = items[k] = sc[k] = eff[k] = 0;
     if (g < ng && shape && m.gs[g] < m.gs[g + 1]) {
       const int members = m.gs[g + 1] - m.gs[g];
-      int most = least[g];
+      int len = shared[g];
       if (m.nlen[m.gs[g]] < 0) {
-        most = 0;  // no row to read the prefix through
-      } else if (shared[g] < 0 || shared[g] > most) {
+        len = 0;  // no row to read the prefix through
+      } else if (len < 0 || len > least[g]) {
         good = false;
-        most = 0;
+        len = 0;
       }
-      eff[k] = min(shared[g], most) / KT * KT;
+      eff[k] = len / KT * KT;
       int pairs, odd;
       row_tiles(members, p, pairs, odd);
       const int tiles = eff[k] / KT;
