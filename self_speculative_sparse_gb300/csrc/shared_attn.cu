@@ -1179,7 +1179,9 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
       at[tid][3] = u * p.Mpad + r;
     }
   } else if (tid >= 32 && tid < 48 && tid - 32 <= tmax) {
-    slots[tid - 32] = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + tid - 32);
+    const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, n + tid - 32);
+    slots[tid - 32] = slot;
+    if (slot < 0) report(p.status, VG_ERR_DEVICE_BOUNDS);  // a page outside the pool: neither read nor written
   }
   __syncthreads();
   // (max, sum) row and O of partial i of a row (from one CTA's partial to the next's two lanes' rows
@@ -1302,6 +1304,7 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
       x *= p.scale_log2;
       const int u = u0 + (lane >> 2);
       if (u <= t) {
+        if (!p.k_new && slots[u] < 0) x = neg_inf();  // (a key that the cache does not have)
         pmax = fmaxf(pmax, x);
         if ((lane & 3) == 0) lgs[wr][u] = x;
       }

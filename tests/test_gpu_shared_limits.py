@@ -62,3 +62,50 @@ def test_a_shared_length_beyond_a_member_is_reported_and_the_group_read_by_itsel
     c.call()
     c.check(status=vb.VG_ERR_DEVICE_BOUNDS, K0=K0, V0=V0)
     assert guards_hold(whole)
+
+
+def attention_without(c, b, missing):
+    """Output and sum of weights times |V| of sequence b's rows in float64, its own rows `missing` left out."""
+    from tests.parity import bf16_to_f64
+    n, t = c.n[b], c.tok[b]
+    G = c.Hq // c.Hkv
+    K = np.concatenate([bf16_to_f64(c.K)[t[:n]], bf16_to_f64(c.kn[b])])
+    V = np.concatenate([bf16_to_f64(c.V)[t[:n]], bf16_to_f64(c.vn[b])])
+    q = bf16_to_f64(c.q[b])
+    out, size = np.zeros_like(q), np.zeros_like(q)
+    for r in range(c.R):
+        use = np.array([i for i in range(n + r + 1) if i - n not in missing])
+        for h in range(c.Hq):
+            s = K[use, h // G] @ q[r, h] / np.sqrt(c.d)
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            out[r, h], size[r, h] = w @ V[use, h // G], w @ np.abs(V[use, h // G])
+    return out, size
+
+
+@pytest.mark.parametrize("append", [True, False])
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+@pytest.mark.parametrize("private,missing", [([40, 32, 60], [0, 1, 2, 3]), ([40, 30, 60], [2, 3])])
+def test_verify_rows_on_a_page_outside_the_pool_are_reported_and_skipped(private, missing, bad, append):
+    # sequence 1's rows begin at (or two tokens before) the page after its prefix's, which it does not have, as
+    # after a pool that ran out; in the second shape there are enough rows for a combine of eight a CTA
+    for others, kw in ((0, dict()), (17, dict(Hq=32, Hkv=8, d=128))):
+        c = Case([3, others], [256, 16], [private, list(range(others))], gamma=3, append=append, **kw)
+        b, n = 1, c.n[1]
+        from tests.parity import bf16_to_f64
+        ref, size = attention_without(c, b, missing if not append else [])
+        K0, V0 = c.K.clone(), c.V.clone()
+        c.table[b, -(-n // 16)] = bad
+        c.call()
+        c.check(skip=[b], status=vb.VG_ERR_DEVICE_BOUNDS, K0=K0, V0=V0)
+        err = np.abs(bf16_to_f64(c.out[b]) - ref)
+        assert (err <= 2.0 ** -8 * (size + 2 * np.abs(ref)) + 2.0 ** -14 * size).all(), err.max()
+        # what has a place was appended, and nothing else was written
+        new = [t[k:] for t, k in zip(c.tok, c.n)]
+        new[b] = new[b][:c.R - len(missing)]
+        if append:
+            assert torch.equal(c.K[torch.from_numpy(new[b]).cuda()], c.kn[b, :c.R - len(missing)])
+        rest = np.setdiff1d(np.arange(c.K.shape[0]), np.concatenate(new) if append else [])
+        rest = torch.from_numpy(rest).cuda()
+        assert torch.equal(c.K[rest].view(torch.int16), K0[rest].view(torch.int16))
+        assert torch.equal(c.V[rest].view(torch.int16), V0[rest].view(torch.int16))
