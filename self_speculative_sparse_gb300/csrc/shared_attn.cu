@@ -21,9 +21,9 @@
 // While one lane's warps run the softmax of their tile, the tensor cores work for the other
 // (P V of its tile, then Q K^T of its next): the lanes' issuers take turns.  P goes back to tensor
 // memory as bf16, over the columns of S, and is the A operand of P V from there: it never passes
-// shared memory.  Rounding P (not its sum) moves an output by at most 2^-8 of sum p |v|, about the
-// size of the output's own rounding; a second product with what the rounding drops would lengthen
-// a step by 1024 of its 2700 cycles.
+// shared memory.  The rows' sums are of the rounded P, so that weights sum to one and the rounding
+// moves an output by at most 2^-8 of sum p |v - out|.  A second product with what the rounding drops
+// lengthens a step by 1024 of its 2700 cycles: only ranges of few keys have it (kLowKeys).
 // Warps: 0-7 and 8-15 the lanes (two threads a row), 16 and 18 the TMA producers, 17 and 19
 // the lanes' MMA issuers; 16 also plans the CTA's runs.
 //
@@ -42,10 +42,17 @@ namespace {
 
 constexpr int KT = kSharedTileKeys;  // keys of a tile, and rows of a lane
 static_assert(KT == 128, "a lane's rows and a tile's keys are the 128 tensor-memory lanes");
-// A row's running max is raised only when a tile exceeds it by more than this (log2 units):
-// P stays below 2^8 and O is rescaled rarely.
-constexpr float kRescaleSlack = 8.f;
+// A row's running max is raised only when the P of one half of a tile, 64 keys, sum to more than this:
+// P stays below 2^8 and O is rescaled rarely.  (The sum is needed anyway: 64 sequences over 16384 shared
+// tokens take 166 us a call so, and 172 with a maximum of every half tile of S beside it.)
+constexpr float kMostSum = 256.f;
 constexpr int kMaxSlots = 12;  // ring slots (K or V tiles) at most
+// A private range of a sequence with at most this many prefix tokens, and a shared range of at most
+// as many, carry P as a bf16 high part plus a bf16 low part (exact to 2^-17), as vg_verify_attn does:
+// with so few keys, rows whose weight sits on two or three of them are likely, and there the rounding of P
+// to one bf16 can pass the output's own.  (The smallest call, two sequences of 512 tokens: 17.3 us, 15.5
+// with P in one part.)
+constexpr int kLowKeys = 1024;
 
 // ---------------------------------------------------------------- the batch's layout
 // Everything the kernels need about lengths and groups, in the workspace: built from the
@@ -326,6 +333,7 @@ struct Run {
   int head[2];        // KV head of each lane
   int r0[2];          // first query row of each lane
   bool priv;
+  bool low;           // P's low part is multiplied too
   int item;           // index of its partials among the shared / private items
 };
 
@@ -335,7 +343,8 @@ struct __align__(16) RunRec {
   int mode, ntiles, tile0, ntok;  // ntiles -1: no further run
   int tok0, row, rows, priv;
   int head[2], r0[2];
-  int unit, pad[3];  // of its partials (for lane 0)
+  int unit;  // of its partials (for lane 0)
+  int low, pad[2];
 };
 static_assert(sizeof(RunRec) == 64, "");
 
@@ -358,6 +367,7 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     r.tok0 = 0;
     r.ntok = m.eff[g];
     r.priv = false;
+    r.low = r.ntok <= kLowKeys;
     r.item = m.itemS[g] + it;
     const int np = p.Hkv * pairs;
     if (it < np) {
@@ -384,6 +394,7 @@ __device__ __forceinline__ Run make_run(const SharedParams& p, const Meta& m, in
     r.tok0 = eff;
     r.ntok = m.nlen[b] - eff;
     r.priv = true;
+    r.low = m.nlen[b] <= kLowKeys;
     r.item = b * Hp + hp;
     r.mode = 2 * hp + 1 < p.Hkv ? kHeads : kSingle;
     r.head[0] = 2 * hp;
@@ -444,6 +455,18 @@ __device__ __forceinline__ void tc_ld16x3_sync(uint32_t t0, uint32_t t1, uint32_
 #pragma unroll
   for (int i = 0; i < 48; ++i) v[i / 16][i % 16] = __uint_as_float(r[i]);
 }
+// 16 columns, likewise.
+__device__ __forceinline__ void tc_ld16_sync(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 // 64 columns, likewise.
 __device__ __forceinline__ void tc_ld64_sync(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
@@ -456,9 +479,12 @@ __device__ __forceinline__ void tc_ld64_sync(uint32_t taddr, float (&v)[64]) {
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
-// Bit patterns to 32 columns of this thread's lane.
+// Bit patterns to 32 and 16 columns of this thread's lane.
 __device__ __forceinline__ void tc_st32b(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+__device__ __forceinline__ void tc_st16b(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
 // One fp32 value to a column of this thread's lane, and from one (waited for).
 __device__ __forceinline__ void tc_st1(uint32_t taddr, float v) {
@@ -511,13 +537,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
         "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -701,11 +720,11 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     bool ended = false;
     auto plan = [&] {
       if (ended) return true;
-      RunRec out{kPair, -1, 0, 0, 0, 0, 0, 0, {0, 0}, {0, 0}, 0, {0, 0, 0}};
+      RunRec out{kPair, -1, 0, 0, 0, 0, 0, 0, {0, 0}, {0, 0}, 0, 0, {0, 0}};
       while (x < x1 && out.ntiles <= 0) {
         const Run r = make_run(p, m, x, x1);
         out = RunRec{r.mode, r.ntiles, r.tile0, r.ntok, r.tok0, r.row, r.rows, r.priv, {r.head[0], r.head[1]},
-                     {r.r0[0], r.r0[1]}, (cta + r.item) * 2, {0, 0, 0}};
+                     {r.r0[0], r.r0[1]}, (cta + r.item) * 2, r.low, {0, 0}};
       }
       ended = out.ntiles <= 0;
       if (ended) out.ntiles = -1;
@@ -859,13 +878,17 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       release();
       if (end) tc_commit_one(lead, &q_empty[w]);
     };
-    // O (+)= P V from the next use (filled), P written
-    auto pv = [&](bool first, bool end) {
+    // O (+)= P V from the next use (filled), P written (low: its low part too)
+    auto pv = [&](bool first, bool end, bool low) {
       tc_fence_after();
       const uint64_t db = dv + static_cast<uint64_t>(st * (C::TILE_BYTES / 16));
 #pragma unroll
       for (int kk = 0; kk < KT / 16; ++kk)
-        tc_mma_ta_one(lead, to, ts + kk * 8, db + kk * 128, idO, (kk > 0 || !first) ? 1u : 0u);
+        tc_mma_ta_one(lead, to, ts + kk * (low ? 16 : 8), db + kk * 128, idO, (kk > 0 || !first) ? 1u : 0u);
+      if (low) {
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk) tc_mma_ta_one(lead, to, ts + kk * 16 + 8, db + kk * 128, idO, 1u);
+      }
       release();
       if (end) tc_commit_one(lead, &o_full[w]);
     };
@@ -877,6 +900,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       const RunRec* rec = run_at(k);
       if (!rec) break;
       const int ntiles = __shfl_sync(0xffffffffu, rec->ntiles, 0), mode = __shfl_sync(0xffffffffu, rec->mode, 0);
+      const bool low = __shfl_sync(0xffffffffu, rec->low, 0) != 0;
       run_done(k);
       const int last = ntiles - 1;
       if (mode == kSingle && w == 1) {
@@ -912,7 +936,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         if (!ok) break;
         tpar ^= turns;
         ppar ^= 1;
-        pv(n == 0, end);
+        pv(n == 0, end, low);
         skip(1);
         if (!end) {
           qk(n + 1 == last);
@@ -928,7 +952,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
     // ---------------------------------------------------------------- softmax lanes
     // Two threads a row: half 0 takes keys 0 .. 63 of each tile, half 1 the others, and each half
     // of the output's columns where those are touched.  They use one running maximum, the row's
-    // maximum at the last time it was raised: while no key exceeds it by more than the slack, a
+    // maximum at the last time it was raised: while no half tile's P sum to more than kMostSum, a
     // thread needs nothing of the other but the word that this holds for both (which the
     // barrier that lets P overwrite S brings along), and the maximum is off the path from S to P.
     constexpr int HK = KT / 2;
@@ -989,7 +1013,6 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         }
         const int valid = left - HK * half;  // keys of this half (64 or more: all)
         uint32_t pk[HK / 2];
-        float ls;
         auto load_s = [&](float (&s)[HK]) {
           tc_ld64_sync(ts + HK * half, s);
           if (valid < HK) {
@@ -1017,25 +1040,25 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           tc_fence_after();
           mx = fmaxf(t, tc_ld1_sync(to_other));
         }
-        while (true) {
-          // P = 2^(s c2 - mx) of this half, its sum (of the fp32 values: a packed add) and maximum
+        float ls = 0.f;
+        for (bool raised = false;; raised = true) {
+          // P = 2^(s c2 - mx) of this half, and its sum, of the bf16 values that P V multiplies: a row's
+          // weights sum to one
           float s[HK];
           load_s(s);
-          float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          float t2[2] = {s[0], s[1]};
+          float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < HK; i += 2) {
-            t2[(i >> 1) & 1] = max3(t2[(i >> 1) & 1], s[i], s[i + 1]);
             const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c2, c2), make_float2(-mx, -mx));
-            const float2 w2 = make_float2(ex2(e.x), ex2(e.y));
-            a2[(i >> 1) & 1] = add2(a2[(i >> 1) & 1], w2);
-            pk[i / 2] = pack_bf16(w2.x, w2.y);
+            pk[i / 2] = pack_bf16(ex2(e.x), ex2(e.y));
+            a4[(i >> 1) & 3] = add_bf16x2_f32(pk[i / 2], a4[(i >> 1) & 3]);
           }
-          ls = (a2[0].x + a2[0].y) + (a2[1].x + a2[1].y);
+          ls = (a4[0] + a4[1]) + (a4[2] + a4[3]);
           // (both threads of each row have read S after the barrier: P may overwrite it)
-          if (!named_bar_or(pair_bar, 64, row < nrows && fmaxf(t2[0], t2[1]) * c2 > mx + kRescaleSlack)) break;
+          if (!named_bar_or(pair_bar, 64, row < nrows && ls > kMostSum) || raised) break;
           // rare: the row's maximum over the whole tile, which both threads of the row read for
-          // themselves, becomes the one in use; then P again
+          // themselves, becomes the one in use; then P again.  (A sum of 64 beyond kMostSum has a P of
+          // 4 or more in it: two above the maximum in use)
           float t = neg_inf();
 #pragma unroll 1
           for (int c0 = 0; c0 < KT; c0 += 32) {
@@ -1045,7 +1068,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
             for (int i = 0; i < 32; ++i) t = fmaxf(t, c0 + i < left ? v[i] : neg_inf());
           }
           t *= c2;
-          const float mn = t > mx + kRescaleSlack ? t : mx;
+          const float mn = t > mx + 1.f ? t : mx;
           // (P V of the lane's previous tile has completed: the commit that brought this S
           // came after it)
           const float alpha = mn != mx ? ex2(mx - mn) : 1.f;
@@ -1060,11 +1083,30 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           }
           mx = mn;
         }
-        l += ls;
-        if (real) {
+        if (real && rec->low != 0) {
+          // P in two parts, over S in place: a step of 16 keys of the product has its high parts in the
+          // first eight of their columns of S and its low parts in the others
+          ls = 0.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < HK; c0 += 16) {
+            float v[16];
+            uint32_t part[16];
+            tc_ld16_sync(ts + HK * half + c0, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float p0 = c0 + 2 * i < valid ? ex2(fmaf(v[2 * i], c2, -mx)) : 0.f;
+              const float p1 = c0 + 2 * i + 1 < valid ? ex2(fmaf(v[2 * i + 1], c2, -mx)) : 0.f;
+              split_bf16(p0, p1, part[i], part[8 + i]);
+              ls = add_bf16x2_f32(part[8 + i], add_bf16x2_f32(part[i], ls));
+            }
+            tc_st16b(ts + HK * half + c0, part);
+          }
+          tc_wait_st();
+        } else if (real) {
           tc_st32b(ts + (HK / 2) * half, pk);
           tc_wait_st();
         }
+        l += ls;
         tc_fence_before();
         __syncwarp();
         if (real && lane == 0) mbar_arrive(&p_full[w]);
