@@ -405,7 +405,8 @@ vg_status vg_shared_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, c
  *   prefix_len     device int32 [B], each in [0, max_len]: tokens in the cache before the rows.
  * A row whose prefix length is out of range is left alone, one whose slot lies outside the
  * cache is not appended (its q is still rotated); both report VG_ERR_DEVICE_BOUNDS.  Any
- * page_size >= 1.  n_rows in [0, 2^24]; uses no workspace; one launch (none for 0 rows).
+ * page_size >= 1.  n_rows in [0, 2^24]; uses no workspace; one launch (none for 0 rows, for which
+ * q, k, v and q_out may be NULL).
  */
 #define VG_ROPE_HALF 0
 #define VG_ROPE_INTERLEAVED 1
@@ -462,7 +463,8 @@ vg_status vg_rope_freqs(int32_t rot_dim, double base, uint32_t scaling, double f
  * request keeps what it had after releases, and so do all later ones that need pages.  Calls
  * that share a pool or a workspace must be ordered on one stream.
  * Workspace: vg_pages_workspace_size bytes (0 on a bad pool), 256-byte aligned, contents
- * arbitrary before and after.  All pointers 16-byte aligned.
+ * arbitrary before and after.  All pointers 16-byte aligned.  A request of no rows (n = 0) does
+ * nothing; its lists may be NULL.
  */
 typedef struct vg_page_pool {
   int32_t* page_table;

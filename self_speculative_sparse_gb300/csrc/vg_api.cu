@@ -951,7 +951,7 @@ vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg
   if (n_rows < 0 || n_rows > (1 << 24)) return fail(VG_ERR_INVALID_ARG, "n_rows=%d outside [0, 2^24]", n_rows);
   if (!row_start && n_rows != s.B * s.R)
     return fail(VG_ERR_INVALID_ARG, "n_rows=%d is not B * (gamma + 1) = %d (no row_start)", n_rows, s.B * s.R);
-  if (!q || !k || !v || !q_out || !prefix_len)
+  if (!prefix_len || (n_rows > 0 && (!q || !k || !v || !q_out)))  // (an empty tensor's address is NULL)
     return fail(VG_ERR_INVALID_ARG, "q, k, v, q_out and prefix_len must be non-NULL");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(prefix_len) ||
       !aligned16(row_start))
@@ -960,7 +960,7 @@ vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg
   if ((st = check_row_stride(k_stride, s.Hkv, s.D, "k_stride")) != VG_OK) return st;
   if ((st = check_row_stride(v_stride, s.Hkv, s.D, "v_stride")) != VG_OK) return st;
   if ((st = check_row_stride(q_out_stride, s.Hq, s.D, "q_out_stride")) != VG_OK) return st;
-  if (q_out == q && q_out_stride != q_stride)
+  if (n_rows > 0 && q_out == q && q_out_stride != q_stride)
     return fail(VG_ERR_INVALID_ARG, "q rotated in place needs q_out_stride == q_stride");
   if (!aligned4(dev_status)) return fail(VG_ERR_INVALID_ARG, "dev_status must be 4-byte aligned");
   if (n_rows == 0) return VG_OK;
@@ -1119,7 +1119,7 @@ vg_status vg_pages_resize(const vg_page_pool* pool, const int32_t* seq, const in
   vg_status st = check_pool(pool);
   if (st != VG_OK) return st;
   if (n < 0 || n > pool->n_seqs) return fail(VG_ERR_INVALID_ARG, "n=%d outside [0, n_seqs=%d]", n, pool->n_seqs);
-  if (!length) return fail(VG_ERR_INVALID_ARG, "length must be non-NULL");
+  if (n > 0 && !length) return fail(VG_ERR_INVALID_ARG, "length must be non-NULL");
   if (!aligned16(seq) || !aligned16(length)) return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   PagesParams p;
   if ((st = check_pages_call(pool, ws, ws_bytes, dev_status, &p)) != VG_OK) return st;
@@ -1145,7 +1145,8 @@ vg_status vg_pages_fork(const vg_page_pool* pool, const vg_kv_cache* caches, int
   if (st != VG_OK) return st;
   if (n < 0 || n > pool->n_seqs) return fail(VG_ERR_INVALID_ARG, "n=%d outside [0, n_seqs=%d]", n, pool->n_seqs);
   if (room < 0) return fail(VG_ERR_INVALID_ARG, "room=%d < 0", room);
-  if (!parent || !child || !length) return fail(VG_ERR_INVALID_ARG, "parent, child and length must be non-NULL");
+  if (n > 0 && (!parent || !child || !length))
+    return fail(VG_ERR_INVALID_ARG, "parent, child and length must be non-NULL");
   if (!aligned16(parent) || !aligned16(child) || !aligned16(length))
     return fail(VG_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   PagesParams p;

@@ -1,0 +1,48 @@
+"""Requests to the batch operators as the Python classes take them, on a host without a GPU: empty ones do
+nothing, and tensors that do not fit are refused before any call."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from self_speculative_sparse_gb300 import binding as vb  # noqa: E402
+from self_speculative_sparse_gb300 import build  # noqa: E402
+from tests.test_abi import A, cache, dims  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+
+
+def make_pool(layers=2, n_seqs=6, n_pages=12, page=4, **kw):
+    from self_speculative_sparse_gb300.runtime import PagePool
+    kv = [tuple(torch.zeros(n_pages * page, 2, 64, dtype=torch.bfloat16) for _ in range(2)) for _ in range(layers)]
+    pool = PagePool(n_seqs, 5, n_pages, page, kw.get("kv", kv))
+    ws = torch.empty(pool.ws.numel() + 256, dtype=torch.uint8)  # (host memory is not always 256-byte aligned)
+    pool.ws = ws[-ws.data_ptr() % 256:][:pool.ws.numel()]
+    return pool
+
+
+def empty():
+    return torch.empty(0, dtype=torch.int32)
+
+
+def test_empty_requests_do_nothing():
+    pool = make_pool()
+    assert empty().data_ptr() == 0
+    pool.resize(empty(), empty(), stream=0)
+    pool.resize(None, empty(), stream=0)
+    pool.fork(empty(), empty(), empty(), 3, stream=0)
+
+
+def test_no_rows_rotate_to_nothing():
+    d, c, r = dims(), cache(), vb.vg_rope(A.addr, 64, 0, 1.0)
+    rows = torch.empty(0, 8, 64, dtype=torch.bfloat16)
+    keys = torch.empty(0, 2, 64, dtype=torch.bfloat16)
+    vb.vg_rope_append(d, c, r, rows, rows.stride(0), keys, keys.stride(0), keys, keys.stride(0), A, 0, A, rows,
+                      rows.stride(0), stream=0)
+    st = vb.load().vg_rope_append(ctypes.byref(d), ctypes.byref(c), ctypes.byref(r), None, 512, None, 128, None, 128,
+                                  A.addr, 0, None, None, 512, None, None)
+    assert st == vb.VG_ERR_INVALID_ARG  # (prefix_len has a length of its own)
