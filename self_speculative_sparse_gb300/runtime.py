@@ -173,14 +173,27 @@ class PagePool:
         K, V = self.layers[layer]
         return vb.make_cache(K, V, None, page_table=self.page_table, page_size=self.page_size)
 
+    def _rows(self, **lists) -> int:
+        """How many rows a request's lists name, after checking that the kernels can read them."""
+        n = lists["length"].numel()
+        for name, t in lists.items():
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.refs.device:
+                raise ValueError(f"{name}: int32 in one dense dimension on {self.refs.device}, not {t.dtype} "
+                                 f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+            if t.numel() != n:
+                raise ValueError(f"{name} has {t.numel()} entries, length {n}")
+        return n
+
     def resize(self, seq: torch.Tensor | None, length: torch.Tensor, stream=None) -> None:
-        """Rows seq (None: the first ones) hold length tokens each; 0 frees a row."""
-        vb.vg_pages_resize(self.pool, seq, length, length.numel(), self.ws, dev_status=self.status, stream=stream)
+        """Rows seq (None: the first ones) hold length tokens each; 0 frees a row.  int32 tensors."""
+        n = self._rows(length=length) if seq is None else self._rows(seq=seq, length=length)
+        vb.vg_pages_resize(self.pool, seq, length, n, self.ws, dev_status=self.status, stream=stream)
 
     def fork(self, parent: torch.Tensor, child: torch.Tensor, length: torch.Tensor, room: int = 0,
              stream=None) -> None:
-        """Rows child become branches of the first length tokens of rows parent."""
-        vb.vg_pages_fork(self.pool, self.caches, self.token_bytes, parent, child, length, length.numel(), room,
+        """Rows child become branches of the first length tokens of rows parent.  int32 tensors."""
+        n = self._rows(parent=parent, child=child, length=length)
+        vb.vg_pages_fork(self.pool, self.caches, self.token_bytes, parent, child, length, n, room,
                          self.ws, dev_status=self.status, stream=stream)
 
     def compact(self, stream=None) -> None:

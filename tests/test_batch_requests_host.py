@@ -46,3 +46,55 @@ def test_no_rows_rotate_to_nothing():
     st = vb.load().vg_rope_append(ctypes.byref(d), ctypes.byref(c), ctypes.byref(r), None, 512, None, 128, None, 128,
                                   A.addr, 0, None, None, 512, None, None)
     assert st == vb.VG_ERR_INVALID_ARG  # (prefix_len has a length of its own)
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+@pytest.fixture
+def no_calls(monkeypatch):
+    """What is refused must be refused before the library is called."""
+    def call(*args, **kw):
+        raise AssertionError("the library was called")
+    for name in ("vg_pages_resize", "vg_pages_fork", "vg_pages_compact", "vg_rope_append", "vg_shared_verify_attn"):
+        monkeypatch.setattr(vb, name, call)
+
+
+BAD_LISTS = {
+    "int64": torch.tensor([1, 2]),
+    "shorter": ints(1),
+    "longer": ints(1, 2, 3),
+    "two dimensions": ints(1, 2).view(2, 1),
+    "apart": ints(1, 0, 2, 0)[::2],
+    "elsewhere": torch.empty(2, dtype=torch.int32, device="meta"),
+}
+
+
+@pytest.mark.parametrize("what", list(BAD_LISTS))
+def test_request_lists_are_checked(no_calls, what):
+    pool, good, bad = make_pool(), ints(1, 2), BAD_LISTS[what]
+    with pytest.raises(ValueError):
+        pool.resize(bad, good)
+    with pytest.raises(ValueError):
+        pool.fork(bad, good, good)
+    with pytest.raises(ValueError):
+        pool.fork(good, bad, good)
+    with pytest.raises(ValueError):
+        pool.fork(good, good, bad)
+    with pytest.raises(ValueError):
+        pool.resize(good, bad)
+    if what not in ("shorter", "longer"):
+        with pytest.raises(ValueError):
+            pool.resize(None, bad)
+
+
+def test_request_lists_that_fit_are_passed_on(monkeypatch):
+    pool, seen = make_pool(), []
+    monkeypatch.setattr(vb, "vg_pages_resize", lambda *a, **kw: seen.append(a[1:4]))
+    monkeypatch.setattr(vb, "vg_pages_fork", lambda *a, **kw: seen.append(a[3:8]))
+    a, b, c = ints(3, 4), ints(0, 1), ints(7, 9)
+    pool.resize(a, c)
+    pool.resize(None, c)
+    pool.fork(b, a, c, 5)
+    assert seen == [(a, c, 2), (None, c, 2), (b, a, c, 2, 5)]
