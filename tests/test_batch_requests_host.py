@@ -98,3 +98,38 @@ def test_request_lists_that_fit_are_passed_on(monkeypatch):
     pool.resize(None, c)
     pool.fork(b, a, c, 5)
     assert seen == [(a, c, 2), (None, c, 2), (b, a, c, 2, 5)]
+
+
+def layer(slots=48, heads=2, d=64, dtype=torch.bfloat16, device="cpu"):
+    return torch.zeros(slots, heads, d, dtype=dtype, device=device)
+
+
+@pytest.mark.parametrize("K,V", [
+    (torch.zeros(48, 2, 2, 64, dtype=torch.bfloat16)[:, 0], layer()),   # K and V of a token side by side
+    (layer(), torch.zeros(48, 2, 2, 64, dtype=torch.bfloat16)[:, 1]),
+    (layer(heads=4)[:, ::2], layer()),
+    (layer(), layer(47)),
+    (layer(), layer(heads=1)),
+    (layer(), layer(dtype=torch.float32)),
+    (layer(), layer(device="meta")),
+])
+def test_layers_that_are_not_dense_or_not_alike_are_refused(K, V):
+    with pytest.raises(ValueError):
+        make_pool(kv=[(K, V)])
+    with pytest.raises(ValueError):
+        make_pool(kv=[(layer(), layer()), (K, V)])
+    with pytest.raises(ValueError):
+        vb.make_caches([(layer(), layer()), (K, V)])
+
+
+def test_layers_with_too_few_slots_are_refused_by_the_call():
+    pool = make_pool(kv=[(layer(47), layer(47))])
+    with pytest.raises(vb.VgError) as e:
+        pool.compact(stream=0)
+    assert e.value.status == vb.VG_ERR_INVALID_ARG
+
+
+def test_layers_may_be_slices_of_one_tensor():
+    kv = torch.zeros(3, 2, 48, 2, 64, dtype=torch.bfloat16)
+    pool = make_pool(kv=[(kv[i, 0], kv[i, 1]) for i in range(3)])
+    assert len(pool.caches) == 3 and pool.caches[2].V == kv[2, 1].data_ptr() and pool.token_bytes == 256
