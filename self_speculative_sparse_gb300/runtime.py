@@ -130,11 +130,16 @@ class LayerState:
         """Rotate the verify rows' q ([B * (gamma + 1)][H_q][d], in place without q_out) and k, and
         append k and v behind the prefixes (then ``verify(append=False)``)."""
         q_out = q if q_out is None else q_out
-        for t in (q, k, v, q_out):  # (only the rows may be apart)
-            if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != t.shape[2]):
-                raise ValueError("q, k, v and q_out: each row's heads must lie together")
+        rows = self.B * (self.gamma + 1)
+        for name, t, heads in (("q", q, self.Hq), ("k", k, self.Hkv), ("v", v, self.Hkv), ("q_out", q_out, self.Hq)):
+            if t.dim() < 2 or t.shape[0] != rows or t[0].numel() != heads * self.d:
+                raise ValueError(f"{name}: {rows} rows of {heads} heads of {self.d}, not {tuple(t.shape)}")
+            if t.dtype != torch.bfloat16 or t.device != self.K.device:
+                raise ValueError(f"{name}: bfloat16 on {self.K.device}, not {t.dtype} on {t.device}")
+            if not t[0].is_contiguous():  # (only the rows may be apart)
+                raise ValueError(f"{name}: each row's heads must lie together")
         vb.vg_rope_append(self.dims, self.cache, rope, q, q.stride(0), k, k.stride(0), v, v.stride(0), None,
-                          q.shape[0], self.prefix_len, q_out, q_out.stride(0), dev_status=self.status, stream=stream)
+                          rows, self.prefix_len, q_out, q_out.stride(0), dev_status=self.status, stream=stream)
 
     def launches_per_iteration(self, select_extra: bool = False, tail_from_device: bool = False) -> int:
         """Kernels one iteration enqueues: the verify kernel and its combine, one selection

@@ -133,3 +133,52 @@ def test_layers_may_be_slices_of_one_tensor():
     kv = torch.zeros(3, 2, 48, 2, 64, dtype=torch.bfloat16)
     pool = make_pool(kv=[(kv[i, 0], kv[i, 1]) for i in range(3)])
     assert len(pool.caches) == 3 and pool.caches[2].V == kv[2, 1].data_ptr() and pool.token_bytes == 256
+
+
+# ------------------------------------------------------------ a layer's rows
+def make_layer(monkeypatch, **kw):
+    import synth
+    from self_speculative_sparse_gb300.runtime import LayerState
+    monkeypatch.setattr(vb, "vg_workspace_size", lambda dims, k: 256)  # (asks the device)
+    w = synth.Workload("rows", B=3, Hq=8, Hkv=2, d=64, gamma=1, k=8, n=20, **kw)
+    return LayerState(w, w.layer_pool(0), device="cpu")
+
+
+def row(heads, rows=6, **kw):
+    return torch.zeros(rows, heads, 64, dtype=kw.get("dtype", torch.bfloat16), device=kw.get("device", "cpu"))
+
+
+BAD_ROWS = {
+    "fewer rows": lambda h: row(h, rows=5),
+    "more rows": lambda h: row(h, rows=7),
+    "a row a sequence": lambda h: row(h).view(3, 2, h, 64),
+    "one dimension": lambda h: row(h).reshape(-1),
+    "fewer heads": lambda h: row(h)[:, :1],
+    "more heads": lambda h: row(h + 1),
+    "float32": lambda h: row(h, dtype=torch.float32),
+    "float16": lambda h: row(h, dtype=torch.float16),
+    "elsewhere": lambda h: row(h, device="meta"),
+    "heads apart": lambda h: row(2 * h)[:, ::2],
+    "elements apart": lambda h: torch.zeros(6, h, 128, dtype=torch.bfloat16)[..., ::2],
+    "heads in another order": lambda h: torch.zeros(6, 64, h, dtype=torch.bfloat16).transpose(1, 2),
+}
+
+
+@pytest.mark.parametrize("what", list(BAD_ROWS))
+def test_rows_to_rotate_are_checked(no_calls, monkeypatch, what):
+    st, rope = make_layer(monkeypatch), vb.vg_rope(A.addr, 64, 0, 1.0)
+    good = dict(q=row(8), k=row(2), v=row(2), q_out=row(8))
+    for name, t in good.items():
+        bad = dict(good, **{name: BAD_ROWS[what](t.shape[1])})
+        with pytest.raises(ValueError, match=name):
+            st.rope_append(rope, **bad)
+
+
+def test_rows_that_fit_are_passed_on(monkeypatch):
+    st, rope, seen = make_layer(monkeypatch), vb.vg_rope(A.addr, 64, 0, 1.0), []
+    monkeypatch.setattr(vb, "vg_rope_append", lambda *a, **kw: seen.append(a[3:]))
+    qkv = torch.zeros(6, 12 * 64, dtype=torch.bfloat16)  # slices of one projection's output
+    q, k, v = qkv.split((512, 128, 128), 1)
+    st.rope_append(rope, q, k, v)
+    st.rope_append(rope, q.view(6, 8, 64), k.view(6, 2, 64), v, q_out=row(8))
+    assert [x[1] for x in seen] == [768, 768] and [x[7] for x in seen] == [6, 6] and [x[10] for x in seen] == [768, 512]
