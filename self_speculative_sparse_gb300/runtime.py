@@ -120,7 +120,10 @@ class LayerState:
 
     def verify_shared(self, groups: vb.vg_prefix_groups, ws: torch.Tensor, stream=None, append: bool = True) -> None:
         """``verify`` for groups that share a prefix (vb.make_groups); ws: scratch of
-        vb.vg_shared_verify_workspace_size(self.dims, groups) bytes.  Fills out_verify and scores0."""
+        vb.vg_shared_verify_workspace_size(self.dims, groups) bytes.  Fills out_verify and scores0: a
+        state with a second mask, whose scores1 would stay those of an earlier call, is refused."""
+        if self.mask1:
+            raise ValueError("verify_shared sums the rows of one mask: make the state without a second one")
         vb.vg_shared_verify_attn(self.dims, self.cache, groups, self.q_verify, self.k_new if append else None,
                                  self.v_new if append else None, self.prefix_len, self.mask0, self.scores0,
                                  self.score_stride, self.out_verify, ws, dev_status=self.status, stream=stream)

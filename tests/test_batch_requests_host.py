@@ -182,3 +182,17 @@ def test_rows_that_fit_are_passed_on(monkeypatch):
     st.rope_append(rope, q, k, v)
     st.rope_append(rope, q.view(6, 8, 64), k.view(6, 2, 64), v, q_out=row(8))
     assert [x[1] for x in seen] == [768, 768] and [x[7] for x in seen] == [6, 6] and [x[10] for x in seen] == [768, 512]
+
+
+def test_a_shared_verification_of_two_masks_is_refused(no_calls, monkeypatch):
+    st = make_layer(monkeypatch, extra_rows="all")
+    assert st.mask1 and st.scores1 is not None
+    with pytest.raises(ValueError, match="mask"):
+        st.verify_shared(vb.vg_prefix_groups(1, None, A.addr), st.ws)
+
+
+def test_a_shared_verification_of_one_mask_is_passed_on(monkeypatch):
+    st, seen = make_layer(monkeypatch), []
+    monkeypatch.setattr(vb, "vg_shared_verify_attn", lambda *a, **kw: seen.append(a))
+    st.verify_shared(vb.vg_prefix_groups(1, None, A.addr), st.ws)
+    assert len(seen) == 1 and seen[0][7] == st.mask0 and seen[0][8] is st.scores0
