@@ -452,8 +452,8 @@ vg_status vg_rope_freqs(int32_t rot_dim, double base, uint32_t scaling, double f
  *   refs        int32 [n_pages]: how often a page is held, 0 (or less): free.
  * One table serves every layer: page p of a layer is its slots p * page_size and on.  A new
  * pool is held = 0 and refs = 0; a page that must never be handed out keeps refs > 0.
- * page_size in [1, 2^20], n_pages * page_size < 2^31, n_seqs <= 65536,
- * n_seqs * pages_per_seq < 2^31.
+ * page_size in [1, 2^20], n_pages <= 2^30, n_pages * page_size < 2^31, n_seqs <= 65536,
+ * pages_per_seq <= 2^30, n_seqs * pages_per_seq < 2^31.
  *
  * Requests are served in order, all releases before any page is handed out, the lowest free
  * pages first: the result depends on the state and the request alone.  Reported on the

@@ -1019,6 +1019,8 @@ vg_status check_pool(const vg_page_pool* p) {
     return fail(VG_ERR_INVALID_ARG, "n_pages=%d of %d tokens outside [1, 2^31) slots", p->n_pages, p->page_size);
   if (p->pages_per_seq < 1 || static_cast<int64_t>(p->n_seqs) * p->pages_per_seq > 0x7fffffffLL)
     return fail(VG_ERR_INVALID_ARG, "pages_per_seq=%d outside [1, 2^31 / n_seqs)", p->pages_per_seq);
+  if (p->n_pages > kMaxPages || p->pages_per_seq > kMaxPages)
+    return fail(VG_ERR_INVALID_ARG, "n_pages=%d or pages_per_seq=%d above 2^30", p->n_pages, p->pages_per_seq);
   return VG_OK;
 }
 

@@ -179,6 +179,9 @@ struct RopeParams {
   int32_t* status;
 };
 
+// Most pages of a pool and most entries of a row: the page kernels step over either in 32 bits, some
+// thousands beyond the end at most.
+constexpr int kMaxPages = 1 << 30;
 // Layers whose K and V one page call copies.
 constexpr int kMaxPageLayers = 128;
 

@@ -196,3 +196,20 @@ def test_a_shared_verification_of_one_mask_is_passed_on(monkeypatch):
     monkeypatch.setattr(vb, "vg_shared_verify_attn", lambda *a, **kw: seen.append(a))
     st.verify_shared(vb.vg_prefix_groups(1, None, A.addr), st.ws)
     assert len(seen) == 1 and seen[0][7] == st.mask0 and seen[0][8] is st.scores0
+
+
+# ------------------------------------------------------------ the largest pools
+@pytest.mark.parametrize("fits,kw", [
+    (True, dict(n_pages=1 << 30, page_size=1)), (False, dict(n_pages=(1 << 30) + 1, page_size=1)),
+    (False, dict(n_pages=(1 << 31) - 1, page_size=1)), (True, dict(n_pages=(1 << 30) - 1, page_size=2)),
+    (False, dict(n_pages=1 << 30, page_size=2)),
+    (True, dict(n_seqs=1, pages_per_seq=1 << 30)), (False, dict(n_seqs=1, pages_per_seq=(1 << 30) + 1)),
+    (False, dict(n_seqs=1, pages_per_seq=(1 << 31) - 1)), (False, dict(n_seqs=2, pages_per_seq=1 << 30)),
+])
+def test_pools_stay_within_what_the_kernels_count_in_32_bits(fits, kw):
+    p = vb.vg_page_pool(**{**dict(page_table=A.addr, held=A.addr, refs=A.addr, n_seqs=8, pages_per_seq=16, n_pages=64,
+                                  page_size=16), **kw})
+    lib = vb.load()
+    assert (lib.vg_pages_workspace_size(ctypes.byref(p)) > 0) == fits
+    if not fits:
+        assert lib.vg_pages_resize(ctypes.byref(p), A.addr, A.addr, 1, A.addr, 1 << 40, None, None) == vb.VG_ERR_INVALID_ARG
