@@ -628,7 +628,9 @@ cudaError_t launch_pages_request(const PagesParams& p, const PageLayers& layers,
 cudaError_t launch_pages_compact(const PagesParams& p, const PageLayers& layers, int sms, cudaStream_t stream) {
   const cudaError_t e = launch_cluster(pages_compact_kernel, p, stream);
   if (e != cudaSuccess) return e;
-  return launch_copy<true>(p, layers, static_cast<int64_t>(p.n_pages / 2) * page_pieces(p), sms, stream);
+  const int64_t pieces = static_cast<int64_t>(p.n_pages / 2) * page_pieces(p);
+  const int64_t rows = (static_cast<int64_t>(p.n_seqs) * p.pages_per_seq + kCopyThreads - 1) / kCopyThreads;
+  return launch_copy<true>(p, layers, pieces > rows ? pieces : rows, sms, stream);
 }
 
 }  // namespace vg
