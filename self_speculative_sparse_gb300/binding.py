@@ -313,9 +313,20 @@ def _holding(struct, *tensors):
     return struct
 
 
+def _fits(name: str, t, bits: int, least: int, dim: int = 1) -> None:
+    """Refuses a tensor that the kernels cannot read as `least` integers of that many bits, one after another."""
+    if (str(t.dtype) not in (f"torch.int{bits}", f"torch.uint{bits}") or t.dim() != dim or not t.is_contiguous()
+            or t.numel() < least):
+        raise ValueError(f"{name}: at least {least} dense {bits}-bit integers in {dim} dimension(s), not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+
+
 def make_groups(group_start, shared_len) -> vg_prefix_groups:
     """Groups of consecutive sequences and the tokens each shares: int32 tensors group_start
     [n_groups + 1] (None: one group of the whole batch) and shared_len [n_groups]."""
+    _fits("shared_len", shared_len, 32, 1)
+    if group_start is not None:
+        _fits("group_start", group_start, 32, shared_len.shape[0] + 1)
     return _holding(vg_prefix_groups(shared_len.shape[0], ptr(group_start), ptr(shared_len)), group_start, shared_len)
 
 
@@ -354,7 +365,8 @@ def vg_rope_freqs(rot_dim: int, base: float, scaling: int = VG_ROPE_PLAIN, facto
 
 
 def make_rope(freq, rot_dim: int, layout: int = VG_ROPE_HALF, mscale: float = 0.0) -> vg_rope:
-    """The rotation of vg_rope_append; freq: the frequencies on the device (64-bit integers)."""
+    """The rotation of vg_rope_append; freq: its rot_dim / 2 frequencies on the device (64-bit integers)."""
+    _fits("freq", freq, 64, rot_dim // 2)
     return _holding(vg_rope(ptr(freq), rot_dim, layout, mscale), freq)
 
 
@@ -368,6 +380,9 @@ def vg_rope_append(dims, cache, rope: vg_rope, q, q_stride, k, k_stride, v, v_st
 
 def make_pages(page_table, held, refs, page_size: int) -> vg_page_pool:
     """The page pool of int32 tensors page_table [n_seqs][pages_per_seq], held [n_seqs], refs [n_pages]."""
+    _fits("page_table", page_table, 32, 1, dim=2)
+    _fits("held", held, 32, page_table.shape[0])
+    _fits("refs", refs, 32, 1)
     return _holding(vg_page_pool(ptr(page_table), ptr(held), ptr(refs), page_table.shape[0], page_table.shape[1],
                                  refs.shape[0], page_size), page_table, held, refs)
 

@@ -213,3 +213,36 @@ def test_pools_stay_within_what_the_kernels_count_in_32_bits(fits, kw):
     assert (lib.vg_pages_workspace_size(ctypes.byref(p)) > 0) == fits
     if not fits:
         assert lib.vg_pages_resize(ctypes.byref(p), A.addr, A.addr, 1, A.addr, 1 << 40, None, None) == vb.VG_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------ structs made from tensors
+def test_groups_have_lists_of_the_right_lengths_and_type():
+    g = vb.make_groups(ints(0, 2, 5), ints(7, 9))
+    assert g.n_groups == 2 and vb.make_groups(None, ints(4)).n_groups == 1
+    assert vb.make_groups(ints(0, 2, 5, 0, 0), ints(7, 9)).n_groups == 2  # (a buffer for more)
+    for start, shared in [(ints(0, 5), ints(7, 9)), (ints(), ints()), (torch.tensor([0, 2, 5]), ints(7, 9)), (ints(0, 2, 5), torch.tensor([7, 9])),
+                          (ints(0, 0, 2, 0, 5)[::2], ints(7, 9)), (ints(0, 2, 5), ints(7, 0, 9)[::2]),
+                          (ints(0, 2, 5), ints(7, 9).view(2, 1))]:
+        with pytest.raises(ValueError):
+            vb.make_groups(start, shared)
+
+
+def test_a_rotation_has_all_its_frequencies():
+    freq = torch.from_numpy(vb.vg_rope_freqs(64, 10000.0).view("int64"))
+    assert vb.make_rope(freq, 64).rot_dim == 64
+    assert vb.make_rope(torch.from_numpy(vb.vg_rope_freqs(64, 10000.0)), 64).rot_dim == 64
+    for bad, rot in [(freq, 66), (freq[:31], 64), (freq.double(), 64), (freq.to(torch.int32), 64),
+                     (torch.zeros(64, dtype=torch.int64)[::2], 64)]:
+        with pytest.raises(ValueError):
+            vb.make_rope(bad, rot)
+
+
+def test_a_pool_has_a_count_for_every_row():
+    table, held, refs = torch.full((6, 5), -1, dtype=torch.int32), ints(0, 0, 0, 0, 0, 0), ints(0, 0, 0)
+    p = vb.make_pages(table, held, refs, 16)
+    assert (p.n_seqs, p.pages_per_seq, p.n_pages) == (6, 5, 3)
+    for bad in [(table, held[:5], refs), (table.long(), held, refs), (table, held.long(), refs), (table, held, refs.long()),
+                (table.t(), held[:5], refs), (table[:, :4], held, refs), (table, held, ints(0, 0, 0, 0)[::2]),
+                (table.view(6, 5, 1), held, refs)]:
+        with pytest.raises(ValueError):
+            vb.make_pages(*bad, 16)
