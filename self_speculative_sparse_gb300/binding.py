@@ -204,8 +204,9 @@ def make_cache(K, V, seq_offset, capacity_slots: int | None = None, page_table=N
     (int32 [B][pages_per_seq] tensor)."""
     cap = capacity_slots if capacity_slots is not None else K.shape[0]
     if page_table is None:
-        return vg_kv_cache(ptr(K), ptr(V), ptr(seq_offset), cap, None, 0, 0)
-    return vg_kv_cache(ptr(K), ptr(V), ptr(seq_offset), cap, ptr(page_table), page_size, page_table.shape[1])
+        return _holding(vg_kv_cache(ptr(K), ptr(V), ptr(seq_offset), cap, None, 0, 0), K, V, seq_offset)
+    return _holding(vg_kv_cache(ptr(K), ptr(V), ptr(seq_offset), cap, ptr(page_table), page_size,
+                                page_table.shape[1]), K, V, seq_offset, page_table)
 
 
 def vg_sparse_draft_launches(dims: vg_dims, k_stride: int, tail_len_max: int = 0) -> int:

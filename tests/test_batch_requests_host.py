@@ -246,3 +246,22 @@ def test_a_pool_has_a_count_for_every_row():
                 (table.view(6, 5, 1), held, refs)]:
         with pytest.raises(ValueError):
             vb.make_pages(*bad, 16)
+
+
+def test_structs_keep_their_tensors():
+    import gc
+    import weakref
+    pool = make_pool()
+    c = pool.cache(1)
+    refs = [weakref.ref(t) for t in (*pool.layers[1], pool.page_table)]
+    del pool
+    gc.collect()
+    assert [r() is not None for r in refs] == [True] * 3 and c.page_table == refs[2]().data_ptr()
+    del c
+    gc.collect()
+    assert all(r() is None for r in refs)
+    t = [torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int64)]
+    c = vb.make_cache(*t)
+    refs = [weakref.ref(x) for x in t]
+    del t
+    assert [r().data_ptr() for r in refs] == [c.K, c.V, c.seq_offset]
