@@ -432,7 +432,7 @@ vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *                   original context keeps f_i if r >= fast, gets f_i / factor if r <= slow, and
  *                   a blend linear in r between.  (A common choice of mscale beside it is
  *                   0.1 ln(factor) + 1.)
- * base > 0, factor > 0 (finite), every resulting f_i below 2pi; RAMP: orig_len > 0 and
+ * base > 0, factor > 0 (finite, the base of BASE too), every f_i below 2pi; RAMP: orig_len > 0 and
  * 0 <= slow < fast.  Arguments that a kind does not name are ignored.  No device needed.
  */
 #define VG_ROPE_PLAIN 0u

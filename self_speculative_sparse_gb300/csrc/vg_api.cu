@@ -917,6 +917,8 @@ vg_status vg_rope_freqs(int32_t rot_dim, double base, uint32_t scaling, double f
       (!(orig_len > 0) || !std::isfinite(orig_len) || !(slow >= 0) || !(fast > slow) || !std::isfinite(fast)))
     return fail(VG_ERR_INVALID_ARG, "ramp scaling needs orig_len > 0 and 0 <= slow < fast");
   if (scaling == VG_ROPE_BASE && rot_dim > 2) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  if (!(base > 0) || !std::isfinite(base))
+    return fail(VG_ERR_INVALID_ARG, "the base scaled by factor is outside the range of a double");
   const double kTwoPi = 6.283185307179586476925;
   for (int pass = 0; pass < 2; ++pass) {  // checked first, so that an error leaves freq alone
     for (int i = 0; i < rot_dim / 2; ++i) {

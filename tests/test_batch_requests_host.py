@@ -265,3 +265,12 @@ def test_structs_keep_their_tensors():
     refs = [weakref.ref(x) for x in t]
     del t
     assert [r().data_ptr() for r in refs] == [c.K, c.V, c.seq_offset]
+
+
+@pytest.mark.parametrize("base,factor", [(1e300, 1e20), (10000.0, 1e308), (1e-300, 1e-30)])
+def test_a_base_that_its_factor_takes_out_of_range_is_refused(base, factor):
+    with pytest.raises(vb.VgError) as e:  # (its frequencies would all be zero, or infinite)
+        vb.vg_rope_freqs(64, base, vb.VG_ROPE_BASE, factor)
+    assert e.value.status == vb.VG_ERR_INVALID_ARG
+    if base > 1:
+        assert vb.vg_rope_freqs(64, base, vb.VG_ROPE_PLAIN, factor)[0] > 0
