@@ -106,7 +106,7 @@ __device__ __forceinline__ bool seq_len_ok(const VerifyParams& p, int b, int n) 
 
 // The key / value row of verify row u of sequence b (prefix length n), KV head g: from
 // the inputs when given, else from the cache slot after the prefix (null if that slot
-// is outside the cache).
+// is outside the cache: the combine reports it, and the key gets no weight).
 template <int D>
 __device__ __forceinline__ const __nv_bfloat16* verify_row(const VerifyParams& p, const __nv_bfloat16* fresh,
                                                            const __nv_bfloat16* cache, int b, int n, int u, int g) {
@@ -708,6 +708,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) verify_combine_kernel(c
   constexpr int NB = D == 128 ? 4 : 8;  // partial rows per round of loads (two rounds in registers)
   __shared__ float lgs[kCombineWarps][16];               // a warp's causal logits (log2 units)
   __shared__ __align__(16) __nv_bfloat16 kvs[2][16][D];  // the verify rows' keys and values
+  __shared__ bool gone[16];                              // rows whose slot is outside the cache
   pdl_launch_dependents();  // the selection kernel may start its prologue
   pdl_wait();
   const int* cum = p.meta;
@@ -773,6 +774,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) verify_combine_kernel(c
       const __nv_bfloat16* row = which ? verify_row<D>(p, p.v_new, p.V, b, n, u, g) : verify_row<D>(p, p.k_new, p.K, b, n, u, g);
       reinterpret_cast<uint4*>(&kvs[which][u][0])[c] =
           row ? reinterpret_cast<const uint4*>(row)[c] : make_uint4(0u, 0u, 0u, 0u);
+      if (which == 0 && c == 0) {
+        gone[u] = row == nullptr;
+        if (row == nullptr) report(p.status, VG_ERR_DEVICE_BOUNDS);
+      }
     }
     float pm = NEG, pl = 0.f;
     float va[NB][PER], vb[NB][PER];
@@ -796,7 +801,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) verify_combine_kernel(c
       for (int e = 0; e < PER; ++e) acc += qv[e] * bf2f(kvs[0][u][lane * PER + e]);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      acc *= p.scale_log2;
+      acc = gone[u] ? NEG : acc * p.scale_log2;
       mc = fmaxf(mc, acc);
       if (lane == 0) lg[u] = acc;
     }
@@ -860,6 +865,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) verify_combine_kernel(c
           p.K[dst + e] = kvs[0][t][lane * PER + e];
           p.V[dst + e] = kvs[1][t][lane * PER + e];
         }
+      } else if (lane == 0) {
+        report(p.status, VG_ERR_DEVICE_BOUNDS);
       }
     }
     return;
@@ -958,6 +965,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 4) verify_combine_narrow_kerne
   constexpr int PD = D / 32;                        // elements of a dot product per lane
   __shared__ __align__(16) __nv_bfloat16 sq[RPC][D];        // this CTA's query rows
   __shared__ __align__(16) __nv_bfloat16 skv[2][kMaxR][D];  // the verify rows' keys and values
+  __shared__ bool gone[kMaxR];                              // rows whose slot is outside the cache
   __shared__ int smeta[4];
   pdl_launch_dependents();  // the selection kernel may start its prologue
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -987,6 +995,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 4) verify_combine_narrow_kerne
       const __nv_bfloat16* row = which ? verify_row<D>(p, p.v_new, p.V, b, n, u, g) : verify_row<D>(p, p.k_new, p.K, b, n, u, g);
       reinterpret_cast<uint4*>(&skv[which][u][0])[c] =
           row ? reinterpret_cast<const uint4*>(row)[c] : make_uint4(0u, 0u, 0u, 0u);
+      if (which == 0 && c == 0) {
+        gone[u] = row == nullptr;
+        if (row == nullptr) report(p.status, VG_ERR_DEVICE_BOUNDS);
+      }
     }
     for (int e = tid; e < RPC * CH; e += kNarrowThreads) {
       const int rr = e / CH, c = e - rr * CH;
@@ -1015,13 +1027,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 4) verify_combine_narrow_kerne
           for (int e = 0; e < PD; ++e) acc += qv[e] * bf2f(skv[0][u][lane * PD + e]);
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-          lg[u] = acc * p.scale_log2;
+          lg[u] = gone[u] ? NEG : acc * p.scale_log2;
           mc = fmaxf(mc, lg[u]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kMaxR; ++u) {
-        if (u <= t) {
+        if (u <= t && lg[u] != NEG) {
           const float w = ex2(lg[u] - mc);
           lc += w;
           oc += w * bf2f(skv[1][u][d]);
@@ -1061,7 +1073,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 4) verify_combine_narrow_kerne
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float Mn = fmaxf(Mr, mx);
-      const float sc = ex2(Mr - Mn);  // Mr is finite: the causal part has at least one key
+      const float sc = Mr != NEG ? ex2(Mr - Mn) : 0.f;  // (NEG: none of the row's own keys is in the cache)
       acc *= sc;
       lr *= sc;
       Mr = Mn;
@@ -1083,6 +1095,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 4) verify_combine_narrow_kerne
         const size_t dst = (slot * p.Hkv + g) * D + d;
         p.K[dst] = skv[0][t][d];
         p.V[dst] = skv[1][t][d];
+      } else if (lane == 0) {
+        report(p.status, VG_ERR_DEVICE_BOUNDS);
       }
     }
     return;
