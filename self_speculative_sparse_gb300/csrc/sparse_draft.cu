@@ -82,15 +82,18 @@ __device__ __forceinline__ int tail_len_of(const DraftParams& p, int b) {
 }
 
 // Appends the current draft token's key and value of KV head g of sequence b at slot
-// tail_start + tail_len - 1 (threads t, t + nt, ... of a group; skipped, never
-// faulted, if out of range).
+// tail_start + tail_len - 1 (threads t, t + nt, ... of a group; skipped and reported, never
+// faulted, if the slot is outside the cache).
 template <int D>
 __device__ __forceinline__ void append_token(const DraftParams& p, int b, int g, int t, int nt) {
   const int ts = p.tail_start[b];
   const int tl = tail_len_of(p, b);
   if (!(ts >= 0 && tl >= 1 && tl <= kDraftMaxTail)) return;
   const int64_t slot = kv_slot<true>(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, ts + tl - 1);
-  if (slot < 0) return;
+  if (slot < 0) {
+    if (t == 0) report(p.status, VG_ERR_DEVICE_BOUNDS);
+    return;
+  }
   const size_t dst = (slot * p.Hkv + g) * D;
   const size_t src = (static_cast<size_t>(b) * p.Hkv + g) * D;
   for (int c = t; c < D / 8; c += nt) {
@@ -493,6 +496,7 @@ __global__ void __launch_bounds__(NW * 32) draft_combine_kernel(const DraftParam
     if (ts >= 0 && tl >= 1 && tl <= kDraftMaxTail) {
       const int64_t slot = kv_slot<true>(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, ts + tl - 1);
       if (slot >= 0) adst = (slot * p.Hkv + g) * D;
+      else if (tid == 0) report(p.status, VG_ERR_DEVICE_BOUNDS);
     }
   }
   // The next draft step may start its prologue now.  A step with a settled selection
