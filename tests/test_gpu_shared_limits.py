@@ -109,3 +109,39 @@ def test_verify_rows_on_a_page_outside_the_pool_are_reported_and_skipped(private
         rest = torch.from_numpy(rest).cuda()
         assert torch.equal(c.K[rest].view(torch.int16), K0[rest].view(torch.int16))
         assert torch.equal(c.V[rest].view(torch.int16), V0[rest].view(torch.int16))
+
+
+# With d = 128 a batch's layout (5 (n_groups + 1) + 4 B + 2 integers) takes the fifth tile's place from about 86
+# sequences on: the attention kernel's ring then has four, the fewest that its waits allow.
+FOUR_TILES = {
+    "two_heads_a_step": dict(members=[128], shared=[1500], private=[[(29 * i) % 400 for i in range(128)]], Hq=4, Hkv=4),
+    "one_kv_head": dict(members=[90], shared=[700], private=[[(31 * i) % 300 for i in range(90)]], Hq=1, Hkv=1, gamma=0),
+    "odd_kv_heads": dict(members=[60, 40], shared=[900, 128], private=[[(37 * i) % 500 for i in range(60)], [3] * 40],
+                         Hq=6, Hkv=3, gamma=2),
+    "row_tile_pairs": dict(members=[128], shared=[1300], private=[[(41 * i) % 260 for i in range(128)]], Hq=16, Hkv=4,
+                           gamma=3, page=64),
+    "many_groups": dict(members=[3] * 40, shared=[128 + 50 * i for i in range(40)], private=[[0, 129, 257]] * 40, Hq=8,
+                        Hkv=2, gamma=1),
+    "slot_pool": dict(members=[100], shared=[600], private=[[(17 * i) % 300 for i in range(100)]], Hq=8, Hkv=4, page=0),
+    "long_private": dict(members=[50, 50], shared=[300, 0], private=[[(97 * i) % 3000 for i in range(50)], [40 * i for i in range(50)]],
+                         Hq=8, Hkv=2, gamma=3),
+    "largest_batch": dict(members=[1000, 24], shared=[300, 130], private=[[(37 * i) % 150 for i in range(1000)], [5] * 24],
+                          Hq=2, Hkv=2),
+}
+
+
+@pytest.mark.parametrize("name", list(FOUR_TILES))
+def test_a_ring_of_four_tiles(name):
+    kw = dict(d=128, page=16, scores=name != "long_private")
+    kw.update(FOUR_TILES[name])
+    c = Case(**kw)
+    assert 5 * (len(c.members) + 1) + 4 * c.B + 2 > 360
+    K0, V0 = c.K.clone(), c.V.clone()
+    c.call()
+    first = c.out.clone()
+    c.check(K0=K0, V0=V0)
+    c.K.copy_(K0)
+    c.V.copy_(V0)
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), c.out.view(torch.int16))
