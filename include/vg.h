@@ -197,8 +197,8 @@ vg_status vg_window_select(const int32_t* len, int32_t B, int32_t max_len, int32
  *   tail_start, tail_len  device int32 [B]   out  bf16 [B][H_q][d]
  *   flags  0, or VG_DRAFT_SELECTION_SETTLED (below); other bits are VG_ERR_INVALID_ARG.
  */
-/* The caller vouches that idx, count, seq_offset, tail_start, tail_len and the cache
- * entries at the selected positions were all written before the kernel that precedes
+/* The caller vouches that idx, count, seq_offset or page_table, tail_start, tail_len and the
+ * cache entries at the selected positions were all written before the kernel that precedes
  * this call in the stream began.  That holds for every draft step of a phase after the
  * first: the selection is made once per verification and the steps in between only
  * append draft tokens (Vegas §2 step 3).  The call then starts gathering the selected
@@ -354,7 +354,8 @@ vg_status vg_accept(int32_t B, int32_t gamma, int32_t V, const float* p_logits, 
  *                        are read where the group's first member has them; a remainder past a
  *                        multiple of 128 tokens is read where each member has it, so every
  *                        member's own table row (or slots) must hold all of its tokens, as
- *                        after vg_pages_fork.
+ *                        after vg_pages_fork.  A bad page of the first member among them is a
+ *                        failed check of every member.
  *   row_mask, scores     as row_mask0, scores0 of vg_verify_attn: scores for every prefix entry
  *                        of every sequence, shared ones included; both 0 / NULL to leave out
  *   others               as vg_verify_attn (page_size 8, 16, 32 or a multiple of 64)
@@ -431,7 +432,8 @@ vg_status vg_rope_append(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *   VG_ROPE_RAMP    by parts: a pair that turns r = orig_len * f_i / 2pi times within the
  *                   original context keeps f_i if r >= fast, gets f_i / factor if r <= slow, and
  *                   a blend linear in r between.  (A common choice of mscale beside it is
- *                   0.1 ln(factor) + 1.)
+ *                   0.1 ln(factor) + 1.)  A blend linear in the pair's index i, as some models
+ *                   were trained with, is another: fill freq by that formula.
  * base > 0, factor > 0 (finite, the base of BASE too), every f_i below 2pi; RAMP: orig_len > 0 and
  * 0 <= slow < fast.  Arguments that a kind does not name are ignored.  No device needed.
  */

@@ -23,17 +23,17 @@
 // memory as bf16, over the columns of S, and is the A operand of P V from there: it never passes
 // shared memory.  The rows' sums are of the rounded P, so that weights sum to one and the rounding
 // moves an output by at most 2^-8 of sum p |v - out|.  A second product with what the rounding drops
-// lengthens a step by 1024 of its 2700 cycles: only ranges of few keys have it (kLowKeys).
+// lengthens a step by 1024 of its 2750 cycles: only ranges of few keys have it (kLowKeys).
 // Warps: 0-7 and 8-15 the lanes (two threads a row), 16 and 18 the TMA producers, 17 and 19
 // the lanes' MMA issuers; 16 also plans the CTA's runs.
 //
 // What bounds it: 2048 cycles of tensor-core work a step of two lanes with d = 128, or 128 KB of
-// keys and values a step in heads mode.  In the middle of a run a pair step takes 2700 cycles,
+// keys and values a step in heads mode.  In the middle of a run a pair step takes 2750 cycles,
 // about the rate at which a plain bf16 product runs on this card; a run's start and end (the first
 // tile's latency, the first maximum, partials of 64 KB a lane) cost it another 8000.  64 sequences of
-// 8 rows and 32 heads over 16384 shared and 100 to 1000 private tokens take it 111 us (140 GFLOP:
-// 1.26 PFLOP/s, 66% of a plain product's rate); 16 of one row over 32768 tokens 37 us
-// (134 MB of shared keys and values: 3.6 TB/s; the first tile is there after 18000 of 67000 cycles).
+// 8 rows and 32 heads over 16384 shared and 100 to 1000 private tokens take it 115 us (140 GFLOP:
+// 1.22 PFLOP/s, 64% of a plain product's rate); 16 of one row over 32768 tokens 38 us
+// (134 MB of shared keys and values: 3.5 TB/s; the first tile is there after 18000 of 69000 cycles).
 #include "vg_common.cuh"
 #include "vg_internal.h"
 
@@ -61,7 +61,8 @@ constexpr int kLowKeys = 1024;
 // of rows (a pair of row tiles of a KV head, or one row tile of two KV heads) and its whole key range.
 // Its steps are its key tiles and, before them, kItemSteps more for what filling a run's pipeline and
 // writing its partials costs a CTA; the attention CTAs split the steps of all items evenly, the shared
-// ones first.  (Attention kernel with 1, 2, 3 and 4 such steps: 131, 117, 110 and 115 us for 64 sequences
+// ones first.  (Attention kernel with 1, 2, 3 and 4 such steps, measured when it summed unrounded weights
+// and was 2% faster: 131, 117, 110 and 115 us for 64 sequences
 // of 16384 shared and 100 to 1000 private tokens, 55, 57, 57 and 58 for eight of 20011 in three groups,
 // 38 for 16 of 32768 with each.)
 constexpr int kItemSteps = kSharedItemSteps;
@@ -1195,8 +1196,8 @@ __global__ void __launch_bounds__(2 * D) shared_combine_kernel(const SharedParam
   const int n = rec.n;
   if (n < 0) return;  // the whole CTA
   if (tid < rows) {
-    // an item's tiles are its steps but the first, and every CTA that owns one of those left a
-    // partial
+    // the first kItemSteps steps of an item have no tile (see make_run); every CTA that owns a later one
+    // left a partial
     const SeqRec tot = reinterpret_cast<const SeqRec*>(p.rec)[p.B];
     const int r = r0 + tid, tiles = rec.eff / KT, ptiles = (n - rec.eff + KT - 1) / KT;
     cnt[tid][0] = cnt[tid][1] = 0;

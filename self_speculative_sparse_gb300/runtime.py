@@ -110,8 +110,8 @@ class LayerState:
     def draft_step(self, s: int, tail_len: torch.Tensor, stream=None, settled: bool | None = None) -> None:
         """Draft step s: attend idx U [n_b, n_b + s], appending draft token s at n_b + s.
 
-        settled (default: s > 0): the selection was made before the kernel preceding this
-        call, as it is for every step of a draft phase after the first."""
+        settled (default: s > 0): the selection was made, and the block table last changed, before
+        the kernel preceding this call, as it is for every step of a draft phase after the first."""
         settled = s > 0 if settled is None else settled
         vb.vg_sparse_draft_attn(self.dims, self.cache, self.q_draft[s], self.k_draft[s], self.v_draft[s], self.idx,
                                 self.count, self.k, self.prefix_len, tail_len, self.out_draft[s], self.ws,
