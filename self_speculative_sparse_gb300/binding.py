@@ -390,16 +390,16 @@ def make_pages(page_table, held, refs, page_size: int) -> vg_page_pool:
 
 def make_caches(layers):
     """The host array of cache structs that the page calls take, from (K, V) tensors of each
-    layer ([capacity_slots][...], all alike and dense: a token's bytes lie together, slot after slot)."""
+    layer ([capacity_slots][...], dense, with the same bytes a slot)."""
     layers = [tuple(kv) for kv in layers]
-    first = layers[0][0]
+    slot = [(t.shape[1:].numel() * t.element_size(), t.device) for kv in layers for t in kv]
     for i, kv in enumerate(layers):
         for name, t in zip("KV", kv):
             if not t.is_contiguous():
                 raise ValueError(f"layer {i}: {name} is not dense: {tuple(t.shape)} with strides {t.stride()}")
-            if t.shape[1:] != first.shape[1:] or t.dtype != first.dtype or t.device != first.device:
-                raise ValueError(f"layer {i}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, not as the first "
-                                 f"layer's K: {first.dtype} {tuple(first.shape)} on {first.device}")
+            if (t.shape[1:].numel() * t.element_size(), t.device) != slot[0]:
+                raise ValueError(f"layer {i}: {name} ({t.dtype} {tuple(t.shape)} on {t.device}) has other slots than "
+                                 f"the first layer's K: {slot[0][0]} bytes on {slot[0][1]}")
         if kv[0].shape[0] != kv[1].shape[0]:
             raise ValueError(f"layer {i}: K has {kv[0].shape[0]} slots, V {kv[1].shape[0]}")
     return _holding((vg_kv_cache * len(layers))(*[make_cache(K, V, None) for K, V in layers]), *layers)

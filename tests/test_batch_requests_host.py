@@ -130,6 +130,7 @@ def test_layers_with_too_few_slots_are_refused_by_the_call():
 
 
 def test_layers_may_be_slices_of_one_tensor():
+    assert len(make_pool(kv=[(layer(), layer().view(48, 128))]).caches) == 1
     kv = torch.zeros(3, 2, 48, 2, 64, dtype=torch.bfloat16)
     pool = make_pool(kv=[(kv[i, 0], kv[i, 1]) for i in range(3)])
     assert len(pool.caches) == 3 and pool.caches[2].V == kv[2, 1].data_ptr() and pool.token_bytes == 256
