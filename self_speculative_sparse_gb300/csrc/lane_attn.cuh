@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
         }
         const int valid = left - HK * half;  // keys of this half (64 or more: all)
         uint64_t bits = ~uint64_t{0};
-        if (TREE && nodes && row < nrows) bits = Plan::bits(p, *rec, rec->r0[w] + row, tok + HK * half);
+        if (TREE && nodes) bits = Plan::bits(p, *rec, rec->r0[w] + row, tok + HK * half);
         uint32_t pk[HK / 2];
         auto load_s = [&](float (&s)[HK]) {
           tc_ld64_sync(ts + HK * half, s);

@@ -33,6 +33,7 @@
 // trees of 64 nodes over 16384 tokens: 217 us, with scores 268 to 279: the warps that multiply the keys with the summed queries
 // are the softmax's).
 #include "lane_attn.cuh"
+#include "tree_bits.h"
 #include "tree_step.h"
 
 namespace vg {
@@ -259,20 +260,7 @@ struct TreePlan {
 
   // Which of the tokens first .. first + 63 of the range query row `row` of the item attends.
   static __device__ __forceinline__ uint64_t bits(const TreeParams& p, const RunRec& r, int row, int first) {
-    const uint64_t* sees = p.visible + (static_cast<size_t>(r.row) * p.R + row / p.G) * p.words;
-    const int u = first - r.n, left = r.ntok - first;
-    uint64_t v;
-    if (u <= -64) {
-      v = ~uint64_t{0};
-    } else if (u < 0) {
-      v = (sees[0] << -u) | ((uint64_t{1} << -u) - 1);
-    } else {
-      const int i = u >> 6, s = u & 63;
-      v = i < p.words ? sees[i] >> s : 0;
-      if (s && i + 1 < p.words) v |= sees[i + 1] << (64 - s);
-    }
-    if (left < 64) v &= left <= 0 ? 0 : (uint64_t{1} << left) - 1;
-    return v;
+    return tree_bits(p.visible, p.R, p.words, p.G, r.row, r.rows, row, r.n, r.ntok, first);
   }
   // Adds to columns col .. col + count - 1 of a node's output, at dst, what its nodes' values hold there that is not finite (slow,
   // for trees that have such values: a weight above 0 makes no other number of them).
