@@ -609,8 +609,8 @@ vg_status vg_tree_build(const int32_t* parent, int64_t parent_stride, const int3
  *              entries at positions >= n_b are left untouched
  *   page_size  8, 16, 32 or a multiple of 64
  * What a row does not attend does not touch it, infinities and NaN among other nodes' keys and values neither.  A sequence
- * whose length, prefix length or room in the cache is out of range is reported as VG_ERR_DEVICE_BOUNDS and gets no
- * output; one with a page outside the pool is reported, its results unspecified.
+ * whose length, prefix length or room in the cache is out of range is reported as VG_ERR_DEVICE_BOUNDS and left alone: its
+ * out, its scores and the cache stay as they were.  One with a page outside the pool is reported, its results unspecified.
  * Workspace: vg_tree_verify_workspace_size(dims, n_nodes) bytes (0 on bad arguments or no device), 256-byte
  * aligned, contents arbitrary.  Launches: 2, one more with k_new or scores.
  */

@@ -48,6 +48,23 @@ struct __align__(16) Split {
   int head[2], r0[2];
 };
 
+// Prefix tokens and nodes of sequence b, and whether the call serves it: lengths in range, tokens of 31 bits (to the end of
+// their last tile), and room for all of them in the cache.  The same answer for all three kernels: what is not served is neither
+// appended nor attended nor scored.
+struct Served {
+  int n, m;
+  bool ok;
+};
+__device__ __forceinline__ Served served(const TreeParams& p, int b) {
+  Served s{p.prefix_len[b], p.tree_len ? p.tree_len[b] : p.R, false};
+  const int64_t off = p.ptab ? 0 : p.seq_offset[b];
+  const int64_t tokens = static_cast<int64_t>(s.n) + s.m;
+  s.ok = s.n >= 0 && s.n <= p.max_len && s.m >= 0 && s.m <= p.R && tokens <= 0x7fffffff - KT &&
+         (p.ptab ? tokens <= static_cast<int64_t>(p.pstride) * p.psize
+                 : off >= 0 && off <= p.capacity && off + tokens <= p.capacity);
+  return s;
+}
+
 struct TreePlan {
   using Params = TreeParams;
   static constexpr bool kTree = true, kScores = false;
@@ -69,15 +86,10 @@ struct TreePlan {
   static __device__ __forceinline__ void load(const TreeParams& p, int* mem, int threads) {
     const Layout l = layout(p, mem);
     for (int b = threadIdx.x; b < p.B; b += threads) {
-      const int n = p.prefix_len[b], m = p.tree_len ? p.tree_len[b] : p.R;
-      const int64_t off = p.ptab ? 0 : p.seq_offset[b];
-      bool ok = n >= 0 && n <= p.max_len && m >= 0 && m <= p.R;
-      const int64_t tokens = static_cast<int64_t>(n) + m;
-      ok = ok && (p.ptab ? tokens <= static_cast<int64_t>(p.pstride) * p.psize
-                         : off >= 0 && off <= p.capacity && off + tokens <= p.capacity);
-      if (!ok && blockIdx.x == 0) report(p.status, VG_ERR_DEVICE_BOUNDS);
-      l.n[b] = n;
-      l.m[b] = ok ? m : 0;
+      const Served x = served(p, b);
+      if (!x.ok && blockIdx.x == 0) report(p.status, VG_ERR_DEVICE_BOUNDS);
+      l.n[b] = x.n;
+      l.m[b] = x.ok ? x.m : 0;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -430,13 +442,14 @@ __global__ void __launch_bounds__(kTreeCombineThreads, 4) tree_combine_kernel(co
   }
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int per = (p.max_len + kScoreChunk - 1) / kScoreChunk;
-    const int b = c / per, i = (c - b * per) * kScoreChunk + 4 * tid, n = p.prefix_len[b];
-    const int m = p.tree_len ? p.tree_len[b] : p.R;
-    if (n < 0 || n > p.max_len || m < 0 || m > p.R || i >= n) continue;
+    const int b = c / per, i = (c - b * per) * kScoreChunk + 4 * tid;
+    const Served seq = served(p, b);
+    const int n = seq.n;
+    if (!seq.ok || i >= n) continue;  // (nobody has left its heads' scores)
     const float* src = p.part_s + static_cast<size_t>(b) * p.Hkv * p.s_stride + i;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = 0; k < (m > 0 ? p.Hkv : 0); ++k) {
+    for (int k = 0; k < (seq.m > 0 ? p.Hkv : 0); ++k) {
       const float4 x = *reinterpret_cast<const float4*>(src + k * p.s_stride);
       sum.x += x.x;
       sum.y += x.y;
@@ -462,10 +475,9 @@ __global__ void __launch_bounds__(kTreePrepThreads) tree_prep_kernel(const TreeP
   const int width = p.Hkv * p.D, tid = threadIdx.x;
   if (static_cast<int>(blockIdx.x) < appends) {
     const int b = blockIdx.x / p.R, t = blockIdx.x - b * p.R;
-    const int n = p.prefix_len[b], m = p.tree_len ? p.tree_len[b] : p.R;
-    if (n < 0 || n > p.max_len || m < 0 || m > p.R || t >= m) return;  // (reported by the attention kernel)
-    if (n > 0x7fffffff - VG_TREE_MAX_NODES) return;
-    const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, static_cast<int64_t>(n) + t);
+    const Served seq = served(p, b);
+    if (!seq.ok || t >= seq.m) return;  // (reported by the attention kernel)
+    const int64_t slot = kv_slot(p.seq_offset, p.ptab, p.psize, p.pstride, p.capacity, b, static_cast<int64_t>(seq.n) + t);
     if (slot < 0) {
       if (tid == 0) report(p.status, VG_ERR_DEVICE_BOUNDS);
       return;
@@ -480,8 +492,8 @@ __global__ void __launch_bounds__(kTreePrepThreads) tree_prep_kernel(const TreeP
     return;
   }
   const int x = blockIdx.x - appends, b = x / p.Hkv, g = x - b * p.Hkv, D = p.D;
-  int m = p.tree_len ? p.tree_len[b] : p.R;
-  if (m < 0 || m > p.R) m = 0;
+  const Served seq = served(p, b);
+  const int m = seq.ok ? seq.m : 0;
   const __nv_bfloat16* q = p.q + (static_cast<size_t>(b) * p.R * p.Hq + g * p.G) * D;  // node 0's rows of the head
   // the sum: thread (s, d) takes column d of every S-th head of the named nodes
   const int S = kTreePrepThreads / D, d = tid % D, s0 = tid / D;
