@@ -597,7 +597,7 @@ vg_status vg_tree_build(const int32_t* parent, int64_t parent_stride, const int3
  *   scores[b][i] = sum over the nodes t < m_b whose bit is set in score_rows[b], over all H_q heads, of
  *                  scale * q[b][t][h] . K_i.
  *
- *   dims       gamma is not read; any G in [1, 16]
+ *   dims       gamma is not read; any G in [1, 16]; max_len below 2^31 - 2048
  *   tree->n_nodes   rows a sequence has in q, k_new, v_new and out, 1 .. VG_TREE_MAX_NODES
  *   tree->len       device int32 [B]: m_b, 0 .. n_nodes; NULL: n_nodes each.  Rows behind are neither
  *                   read for a result nor written.

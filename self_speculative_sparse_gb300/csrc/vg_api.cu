@@ -1440,6 +1440,13 @@ vg_status check_nodes(int32_t n_nodes) {
   return VG_OK;
 }
 
+// Tokens of a sequence, and the last tile's and score chunk's behind them, are counted in 31 bits.
+vg_status check_tree_len(const Shape& s) {
+  constexpr int32_t most = 0x7fffffff - 2048;
+  if (s.max_len > most) return fail(VG_ERR_UNSUPPORTED_SHAPE, "max_len=%d > %d", s.max_len, most);
+  return VG_OK;
+}
+
 struct TreeWs {
   size_t rec, parts_o, parts_ml, zsum, part_s, total;
   int s_stride;
@@ -1498,7 +1505,7 @@ vg_status vg_tree_build(const int32_t* parent, int64_t parent_stride, const int3
 size_t vg_tree_verify_workspace_size(const vg_dims* dims, int32_t n_nodes) {
   g_err.clear();
   Shape s;
-  if (check_dims_no_gamma(dims, &s) != VG_OK || check_nodes(n_nodes) != VG_OK) return 0;
+  if (check_dims_no_gamma(dims, &s) != VG_OK || check_tree_len(s) != VG_OK || check_nodes(n_nodes) != VG_OK) return 0;
   DevInfo di;
   if (device_info(&di) != VG_OK) return 0;
   return tree_ws(s, di.sms).total;
@@ -1512,6 +1519,7 @@ vg_status vg_tree_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, con
   Shape s;
   vg_status st = check_dims_no_gamma(dims, &s);
   if (st != VG_OK) return st;
+  if ((st = check_tree_len(s)) != VG_OK) return st;
   if ((st = check_cache(cache)) != VG_OK) return st;
   if ((st = check_verify_pages(cache)) != VG_OK) return st;
   if (!tree) return fail(VG_ERR_INVALID_ARG, "tree is NULL");
