@@ -672,7 +672,7 @@ vg_status vg_tree_accept(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *   T         0: the largest logit's token, lowest index, with probability 1; finite, above 0 it is taken
  *             to lie in [2^-60, 2^60]
  *   token[r]  the smallest kept v where the running sum of the kept weights, by index, exceeds
- *             u[r] times their total; prob[r] (or NULL) its weight over the total
+ *             u[r] times their total; prob[r] (or NULL) its weight over the total, rounded once
  *   filtered  fp32 [n_rows][V] at filtered_stride, or NULL: l / T of the kept tokens (0 where T is 0),
  *             -inf elsewhere: the logits that vg_accept takes for p and q where drafts and target are
  *             sampled with such parameters
