@@ -670,11 +670,11 @@ vg_status vg_tree_accept(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *             token always);  1 or more: all
  *   min_p     keeps those of weight min_p or more, in [0, 1]
  *   T         0: the largest logit's token, lowest index, with probability 1; finite, above 0 it is taken
- *             to lie in [2^-60, 2^60]
+ *             to lie in [2^-70, 2^70]
  *   token[r]  the smallest kept v where the running sum of the kept weights, by index, exceeds
  *             u[r] times their total; prob[r] (or NULL) its weight over the total, rounded once
- *   filtered  fp32 [n_rows][V] at filtered_stride, or NULL: l / T of the kept tokens (0 where T is 0),
- *             -inf elsewhere: the logits that vg_accept takes for p and q where drafts and target are
+ *   filtered  fp32 [n_rows][V] at filtered_stride, or NULL: l / T of the kept tokens (0 where T is 0), held
+ *             within the finite floats, -inf elsewhere: the logits that vg_accept takes for p and q where drafts and target are
  *             sampled with such parameters
  * A logit of -inf or NaN is no token; +inf counts as the largest finite one of its type.  A row without any token
  * gets token -1, probability 0 and is reported as VG_ERR_DEVICE_BOUNDS; so is one whose T, top_p or min_p is

@@ -219,6 +219,9 @@ __device__ __forceinline__ void keys_of_interval(int b, float top, float steps, 
   hi = b > 0 ? next - 1 : key_of(top);
 }
 
+// A temperature above 0 as it is used, for the weights and for the filtered logits.
+__device__ __forceinline__ float within(float temperature) { return fminf(fmaxf(temperature, 0x1p-70f), 0x1p70f); }
+
 // The place in the order of a logit (its bits) and an index.
 __device__ __forceinline__ uint64_t place_of(uint64_t x) {
   return (static_cast<uint64_t>(~key_of(__uint_as_float(static_cast<uint32_t>(x >> 32)))) << 32) | static_cast<uint32_t>(x);
@@ -624,7 +627,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int rows) {
     sh.powers.lo[tid] = g_powers.lo[tid];
   }
   if (tid == 0) {
-    const double t = greedy ? 1.0 : fmin(fmax(static_cast<double>(temp), 0x1p-60), 0x1p60);
+    const double t = greedy ? 1.0 : static_cast<double>(within(temp));
     sh.per_octave = 1.4426950408889634074 / t;
     sh.steps = static_cast<float>(64 / t);
     if (use_m) sh.log_min_p = t * log(static_cast<double>(min_p));
@@ -1253,12 +1256,15 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int rows) {
     if (p.prob) p.prob[row] = 0.f;
   }
   if (!p.filtered) return;
+  // (a kept logit stays finite: what takes -inf for a token that was cut, and +inf for no distribution, reads these rows)
+  constexpr float kMost = 3.402823466e38f;
+  const float t = within(temp);
   float* dst = p.filtered + row * p.filtered_stride;
   x.each([&](const float (&v)[L], int i) {
     float f[L];
 #pragma unroll
     for (int e = 0; e < L; ++e)
-      f[e] = empty || !x.in(v[e], i + e) ? neg_inf() : greedy ? 0.f : __fdiv_rn(v[e], temp);
+      f[e] = empty || !x.in(v[e], i + e) ? neg_inf() : greedy ? 0.f : fminf(fmaxf(__fdiv_rn(v[e], t), -kMost), kMost);
     if (p.vec_out && i + L <= x.end) {
 #pragma unroll
       for (int e = 0; e < L; e += 4)

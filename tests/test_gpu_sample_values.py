@@ -34,3 +34,34 @@ def test_a_probability_is_rounded_once(V, par):
         assert c.token[r].item() == token
         tol = want * (2.0 ** -24 + 2.0 ** -27 + 2.0 ** -50) + 2.0 ** -40 * (1 + len(kept) * want) * most
         assert abs(c.prob[r].item() - want) <= tol
+
+
+MOST = float(np.finfo(np.float32).max)
+
+
+def filtered(c, r, kept):
+    """The definition: a kept logit over T (taken to lie in [2^-70, 2^70]), one rounding, held within the finite floats."""
+    t = np.float32(min(max(float(c.T[r]), 2.0 ** -70), 2.0 ** 70))
+    ref = np.full(c.V, -np.inf, np.float32)
+    with np.errstate(over="ignore"):
+        ref[kept] = np.clip(np.minimum(c.ref[r][kept], np.float32(MOST)) / t, -MOST, MOST)
+    return ref, float(t)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [50, 30000])
+@pytest.mark.parametrize("T,size,shift", [
+    (1e-38, 3.0, -40.0), (1e-38, 3.0, 40.0), (1e-38, 1e-21, 0.0), (1e-38, 1e-21, -1e-20), (1.4e-45, 1.0, 0.0), (1e-20, 1e-20, 0.0),
+    (1e-10, 1e33, 0.0), (0.25, 3e37, -3e38), (1e-3, 1e37, 0.0), (2.0 ** 65, 2e19, 0.0), (3e38, 1.0, 0.0), (1e25, 1e21, 0.0)])
+@pytest.mark.parametrize("par", [dict(), dict(p=0.8), dict(k=5)])
+def test_filtered_logits_are_finite_at_every_temperature(T, size, shift, V, dtype, par):
+    x = np.clip(logits(3, V, spread=1.0, seed=7) * size + shift, -MOST / 2, MOST / 2)
+    c = Rows(x, T=T, dtype=dtype, seed=2, **par).call()
+    assert c.status.item() == 0
+    k, p = par.get("k", 0), float(np.float32(par.get("p", 1.0)))
+    for r in range(c.n):
+        token, _, kept = fast_row(c.ref[r], float(c.u[r]), filtered(c, r, [])[1], k, p, 0.0)
+        got = c.filtered[r, :V].cpu().numpy()
+        assert np.array_equal(got, filtered(c, r, kept)[0])
+        assert np.isfinite(got[kept]).all()
+        assert c.token[r].item() == token
