@@ -25,7 +25,9 @@
 //   accept_pick_kernel (sampling): one CTA per sequence adds the tile totals in order,
 //     finds the tile where the running sum passes the target and scans that tile alone,
 //     with the same reduction as the tile totals, so the two agree.
-// Logits are read as log2-scaled values (l * log2 e), so every exponential is one ex2.
+// Logits are read as log2-scaled values (l * log2 e), so every exponential is one ex2, relative to the rounded maximum m
+// (which one it is does not matter, as long as all use the same).  Rows whose maximum lies beyond +-2^30, where that rounding would
+// take an exponential out of the floats' range, are weighed without one: logits lie 128 apart there, and all weight is the largest's.
 #include "vg_common.cuh"
 #include "vg_internal.h"
 
@@ -40,11 +42,24 @@ constexpr int kTile = kDecThreads * 4;  // vocabulary entries per tile of the dr
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Stat {
-  float m;   // max of l * log2 e
-  float s;   // sum of exp2(l * log2 e - m)
+  float m;   // max of l * log2 e (scaled())
+  float s;   // sum of exp2(l * log2 e - m) (weight())
   float av;  // the max's logit (for the argmax)
   int ai;    // argmax, lowest index
 };
+
+__device__ __forceinline__ bool far_off(float av) { return fabsf(av) >= 0x1p30f; }
+// The maximum that a row's exponentials are relative to, from its logit: ascending, and no far one near another.
+__device__ __forceinline__ float scaled(float av) {
+  constexpr float kMost = 3.402823466e38f;
+  if (!far_off(av)) return av * kLog2e;
+  return fabsf(av) > kMost ? av : fmaxf(-kMost, fminf(kMost, 2.f * av));
+}
+// A logit's weight relative to the row's largest, of logit av and scaled maximum m.
+__device__ __forceinline__ float weight(float l, float m, float av) {
+  const float e = ex2(l * kLog2e - m);
+  return far_off(av) ? (l == av ? 1.f : 0.f) : e;
+}
 
 __device__ __forceinline__ void merge(Stat& a, const Stat& b) {
   const float NEG = neg_inf();
@@ -124,11 +139,11 @@ __global__ void __launch_bounds__(kStatThreads) accept_stats_kernel(const Accept
       st.ai = index(k);
     }
   }
-  st.m = st.av * kLog2e;
+  st.m = scaled(st.av);
   if (st.av != NEG) {
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) sum += ex2(l[k] * kLog2e - st.m);  // (-inf entries add 0)
+    for (int k = 0; k < kPer; ++k) sum += weight(l[k], st.m, st.av);  // (-inf entries add 0)
     st.s = sum;
   }
   st = warp_merge(st);
@@ -172,7 +187,7 @@ __device__ __forceinline__ float block_scan(float v, float* red, float& before) 
 struct Decision {
   int a, next;
   float pm, ps, qm, qs;
-  int pad[2];
+  float pav, qav;  // the maxima's logits
 };
 
 __global__ void __launch_bounds__(kDecideThreads) accept_decide_kernel(const AcceptParams p) {
@@ -215,8 +230,8 @@ __global__ void __launch_bounds__(kDecideThreads) accept_decide_kernel(const Acc
       } else {
         const float lp = p.p_logits[(static_cast<size_t>(b) * (G + 1) + t) * p.V + x];
         const float lq = p.q_logits[(static_cast<size_t>(b) * G + t) * p.V + x];
-        const float pt = ex2(lp * kLog2e - rs[t].m) / rs[t].s;
-        const float qt = ex2(lq * kLog2e - rs[G + 1 + t].m) / rs[G + 1 + t].s;
+        const float pt = weight(lp, rs[t].m, rs[t].av) / rs[t].s;
+        const float qt = weight(lq, rs[G + 1 + t].m, rs[G + 1 + t].av) / rs[G + 1 + t].s;
         ok = p.u[static_cast<size_t>(b) * G + t] * qt < pt;
       }
     }
@@ -243,8 +258,10 @@ __global__ void __launch_bounds__(kDecideThreads) accept_decide_kernel(const Acc
   d.next = sh[1];
   d.pm = rs[a].m;
   d.ps = rs[a].s;
+  d.pav = rs[a].av;
   d.qm = rej ? rs[G + 1 + a].m : 0.f;
   d.qs = rej ? rs[G + 1 + a].s : 1.f;
+  d.qav = rej ? rs[G + 1 + a].av : 0.f;
   reinterpret_cast<Decision*>(p.dec)[b] = d;
 }
 
@@ -253,7 +270,8 @@ __global__ void __launch_bounds__(kDecideThreads) accept_decide_kernel(const Acc
 struct DrawRow {
   const float* lp;
   const float* lq;
-  float pm, ip, qm, iq;
+  float pm, ip, qm, iq, pav, qav;
+  bool far;
   int V;
 };
 
@@ -266,6 +284,9 @@ __device__ __forceinline__ DrawRow draw_row(const AcceptParams& p, int b, const 
   r.ip = 1.f / d.ps;
   r.qm = d.qm;
   r.iq = 1.f / d.qs;
+  r.pav = d.pav;
+  r.qav = d.qav;
+  r.far = far_off(d.pav) || far_off(d.qav);
   r.V = p.V;
   return r;
 }
@@ -300,6 +321,14 @@ __device__ __forceinline__ void tile_weights(const DrawRow& r, int tile, int tid
     const float pv = in ? ex2(lp[e] * kLog2e - r.pm) * r.ip : 0.f;
     wp[e] = pv;
     wx[e] = (in && r.lq) ? fmaxf(0.f, pv - ex2(lq[e] * kLog2e - r.qm) * r.iq) : 0.f;
+  }
+  if (r.far) {  // (apart from the others: with the choice among the lines above a call of 8 sequences takes 26.0 us, not 25.0)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = v + e < r.V;
+      wp[e] = in ? weight(lp[e], r.pm, r.pav) * r.ip : 0.f;
+      wx[e] = (in && r.lq) ? fmaxf(0.f, wp[e] - weight(lq[e], r.qm, r.qav) * r.iq) : 0.f;
+    }
   }
 }
 
