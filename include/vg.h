@@ -668,7 +668,7 @@ vg_status vg_tree_accept(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *   top_k     keeps the first top_k tokens;  0 or less, or V or more: all
  *   top_p     keeps the shortest first part of those whose weight is at least top_p of theirs (the first
  *             token always);  1 or more: all
- *   min_p     keeps those of weight min_p or more, in [0, 1]
+ *   min_p     keeps those of weight min_p or more;  0 or less: all
  *   T         0: the largest logit's token, lowest index, with probability 1; finite, above 0 it is taken
  *             to lie in [2^-70, 2^70]
  *   token[r]  the smallest kept v where the running sum of the kept weights, by index, exceeds
@@ -678,7 +678,7 @@ vg_status vg_tree_accept(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *             sampled with such parameters
  * A logit of -inf or NaN is no token; +inf counts as the largest finite one of its type.  A row without any token
  * gets token -1, probability 0 and is reported as VG_ERR_DEVICE_BOUNDS; so is one whose T, top_p or min_p is
- * NaN or whose T or min_p is out of range (its filtered is left alone).  u outside [0, 1) counts as the nearer end, NaN as 0.
+ * NaN, whose T is negative or infinite or whose min_p is above 1 (its filtered is left alone).  u outside [0, 1) counts as the nearer end, NaN as 0.
  * Weights are whole numbers of 2^-43 of the largest (an error of at most 2^-28 of themselves and 2^-40 of the largest), their sums
  * exact: the result depends on the inputs alone, not on how a row is split.
  *

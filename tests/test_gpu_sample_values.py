@@ -65,3 +65,15 @@ def test_filtered_logits_are_finite_at_every_temperature(T, size, shift, V, dtyp
         assert np.array_equal(got, filtered(c, r, kept)[0])
         assert np.isfinite(got[kept]).all()
         assert c.token[r].item() == token
+
+
+@pytest.mark.parametrize("m", [0.0, -0.0, -1e-45, -0.5, -float("inf")])
+@pytest.mark.parametrize("V,par", [(300, dict()), (30000, dict(p=0.9)), (30000, dict(k=40))])
+def test_a_min_p_of_0_or_less_is_off(m, V, par):
+    x = logits(3, V, seed=5)
+    on, off = Rows(x, m=m, **par).call(), Rows(x, **par).call()
+    off.params.min_p = None
+    off.call()
+    assert on.status.item() == 0
+    for a, b in ((on.token, off.token), (on.prob, off.prob), (on.filtered, off.filtered)):
+        assert torch.equal(a, b)
