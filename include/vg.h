@@ -631,7 +631,8 @@ vg_status vg_tree_verify_attn(const vg_dims* dims, const vg_kv_cache* cache, con
  * target_tokens[b][i] is the token that the target model continues node i with: drawn from its
  * distribution after node i (vg_sample on the nodes' logits), or the most likely one.  The walk
  * starts at node 0 and goes on to the child (the lowest node) whose draft token is the target's,
- * as long as there is one.  Every token it commits was drawn from the target's distribution
+ * as long as there is one.  A token below 0, as vg_sample gives a row without any, is nobody's: the
+ * walk ends there.  Every token it commits was drawn from the target's distribution
  * given the tokens before it: nothing is lost, whatever was drafted.
  *   parent, parent_stride, len  as vg_tree_build
  *   draft_tokens, target_tokens  int32 [B][n_nodes] (node 0's draft token is not read)

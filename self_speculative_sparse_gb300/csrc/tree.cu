@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeA
   }
   if (tid < kMaxNodes) next[tid] = kMaxNodes;
   __syncthreads();
-  if (tid < n && up[tid] >= 0 && token == tgt[up[tid]]) atomicMin(&next[up[tid]], tid);
+  // (a row without any token draws -1, drafts' rows and the target's: no token that both have)
+  if (tid < n && up[tid] >= 0 && token >= 0 && token == tgt[up[tid]]) atomicMin(&next[up[tid]], tid);
   __syncthreads();
   if (tid == 0) {
     int a = 0;
