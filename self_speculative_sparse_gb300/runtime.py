@@ -227,6 +227,18 @@ class TreeStep:
         self.layers = list(layers)
         dev = self.layers[0][0].device
         self.B, self.Hq, self.Hkv, self.d, self.n_nodes = B, H_q, H_kv, d, n_nodes
+        self.max_len, self.words = max_len, -(-n_nodes // 64)
+        for i, kv in enumerate(self.layers):
+            for name, t in zip("KV", kv):
+                if t.dtype != torch.bfloat16 or t.shape[1:].numel() != H_kv * d:
+                    raise ValueError(f"layer {i}: {name} is {t.dtype} {tuple(t.shape)}: slots of {H_kv} heads of {d} bfloat16")
+        if (seq_offset is None) == (page_table is None):
+            raise ValueError("seq_offset or page_table")
+        self._dense("prefix_len", prefix_len, torch.int32, (B,), dev)
+        if page_table is None:
+            self._dense("seq_offset", seq_offset, torch.int64, (B,), dev)
+        else:
+            self._dense("page_table", page_table, torch.int32, (B, 1), dev)
         self.dims = vb.make_dims(B, H_q, H_kv, d, 0, max_len)
         self.cache = [vb.make_cache(K, V, seq_offset, page_table=page_table, page_size=page_size) for K, V in self.layers]
         self.caches = vb.make_caches(self.layers)
@@ -237,7 +249,7 @@ class TreeStep:
         self.tokens = torch.zeros((B, n_nodes), **i32)
         self.target = torch.zeros((B, n_nodes), **i32)
         self.prob = torch.zeros((B, n_nodes), dtype=torch.float32, device=dev)
-        self.visible = torch.zeros((B, n_nodes, -(-n_nodes // 64)), dtype=torch.int64, device=dev)
+        self.visible = torch.zeros((B, n_nodes, self.words), dtype=torch.int64, device=dev)
         self.position = torch.zeros((1, B * n_nodes), **i32)
         self.path = torch.zeros((B, n_nodes), **i32)
         self.n_accept, self.next_token = torch.zeros(B, **i32), torch.zeros(B, **i32)
@@ -245,6 +257,14 @@ class TreeStep:
         self.tree = vb.make_tree(n_nodes, self.visible, self.len)
         self.at = vb.make_positions(self.position, rows_per_seq=n_nodes, seq_rows=self.len)
         self.ws = torch.empty(vb.vg_tree_verify_workspace_size(self.dims, n_nodes), dtype=torch.uint8, device=dev)
+
+    @staticmethod
+    def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, least: tuple, device) -> None:
+        """Refuses a tensor that is not of that type and device, dense, and in each dimension at least as long."""
+        if (t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(least)
+                or any(n < m for n, m in zip(t.shape, least))):
+            raise ValueError(f"{name}: dense {dtype} of at least {least} on {device}, not {t.dtype} {tuple(t.shape)} "
+                             f"with strides {t.stride()} on {t.device}")
 
     def _rows(self, name: str, t: torch.Tensor, heads: int) -> None:
         """Refuses rows that the kernels cannot read: [B * n_nodes] of heads * d together, or [B][n_nodes] dense."""
@@ -272,11 +292,24 @@ class TreeStep:
 
     def verify(self, layer: int, q: torch.Tensor, out: torch.Tensor, score_rows: torch.Tensor | None = None,
                scores: torch.Tensor | None = None, stream=None) -> None:
-        """Attention of the nodes over prefix and ancestors (both in the cache), with the prefix's scores."""
+        """Attention of the nodes over prefix and ancestors (both in the cache).  With scores (float32 [B][max_len or more])
+        the summed logits of the prefix, of the nodes that score_rows names (int64 [B][words], bits)."""
         for name, t in (("q", q), ("out", out)):
             self._rows(name, t, self.Hq)
             if not t.is_contiguous():
                 raise ValueError(f"{name}: dense, not with strides {t.stride()}")
+        if (score_rows is None) != (scores is None):
+            raise ValueError("score_rows and scores: both or neither")
+        if scores is not None:
+            dev = self.visible.device
+            self._dense("score_rows", score_rows.view(torch.int64) if score_rows.dtype == torch.uint64 else score_rows,
+                        torch.int64, (self.B, self.words), dev)
+            if score_rows.shape[1] != self.words:
+                raise ValueError(f"score_rows: rows of {self.words} words, not {score_rows.shape[1]}")
+            if (scores.dtype != torch.float32 or scores.device != dev or scores.dim() != 2 or scores.shape[0] < self.B
+                    or scores.shape[1] < self.max_len or (scores.shape[1] > 1 and scores.stride(1) != 1)):
+                raise ValueError(f"scores: {self.B} rows of float32, {self.max_len} or more together, on {dev}, not "
+                                 f"{scores.dtype} {tuple(scores.shape)} with strides {scores.stride()} on {scores.device}")
         vb.vg_tree_verify_attn(self.dims, self.cache[layer], self.tree, q, None, None, self.prefix_len, score_rows, scores,
                                scores.stride(0) if scores is not None else 0, out, self.ws, dev_status=self.status,
                                stream=stream)
@@ -285,8 +318,14 @@ class TreeStep:
         """The target's token after every node, from its logits ([B * n_nodes][V] float32 or bfloat16).  params: a set
         for each sequence, rows_per_set = n_nodes and set_rows = len (or one for each node)."""
         rows = self.B * self.n_nodes
-        if logits.dim() != 2 or logits.shape[0] != rows or logits.stride(1) != 1 or u.numel() != rows:
-            raise ValueError(f"logits of {rows} rows and as many u, not {tuple(logits.shape)} and {tuple(u.shape)}")
+        dev = self.visible.device
+        if (logits.dim() != 2 or logits.shape[0] != rows or logits.stride(1) != 1 or u.numel() != rows
+                or not u.is_contiguous()):
+            raise ValueError(f"logits of {rows} rows and as many dense u, not {tuple(logits.shape)} and {tuple(u.shape)} "
+                             f"with strides {u.stride()}")
+        for t in (logits, u, *(t for t in getattr(params, "tensors", ()) if t is not None)):
+            if t.device != dev:
+                raise ValueError(f"logits, u and params on {dev}, not {t.device}")
         if params.rows_per_set not in (self.n_nodes, 1):
             raise ValueError(f"params of {params.rows_per_set} rows a set: {self.n_nodes} (a sequence's nodes) or 1")
         kind = {torch.float32: vb.VG_LOGITS_FP32, torch.bfloat16: vb.VG_LOGITS_BF16}.get(logits.dtype)
