@@ -608,6 +608,9 @@ vg_status vg_tree_build(const int32_t* parent, int64_t parent_stride, const int3
  *   score_rows device uint64 [B][words] or NULL;  scores  fp32 [B][score_stride], given iff score_rows is;
  *              entries at positions >= n_b are left untouched
  *   page_size  8, 16, 32 or a multiple of 64
+ * Logits, maxima, sums and outputs are fp32 up to the one rounding of out to bf16.  Where a sequence has more than 1024 tokens, a
+ * key's weight is rounded to bf16 for its product with V, and so in the sum that it is divided by: that moves an output by at
+ * most 2^-8 of sum p |v - out| (2.3e-3 of it in norm, its own rounding included, where that alone is 1.7e-3).
  * What a row does not attend does not touch it, infinities and NaN among other nodes' keys and values neither.  A sequence
  * whose length, prefix length or room in the cache is out of range is reported as VG_ERR_DEVICE_BOUNDS and left alone: its
  * out, its scores and the cache stay as they were.  One with a page outside the pool is reported, its results unspecified.
@@ -691,7 +694,7 @@ vg_status vg_tree_accept(const vg_dims* dims, const vg_kv_cache* cache, const vg
  *                is read or written for the others (out of [0, rows_per_set]: reported, none is)
  *   u            fp32 [n_rows];  token  int32 [n_rows];  prob  fp32 [n_rows] or NULL
  * 1 <= V <= 2^20, 0 <= n_rows <= 2^20.  Workspace: vg_sample_workspace_size bytes (0 on bad arguments),
- * 256-byte aligned, contents arbitrary.
+ * 256-byte aligned, contents arbitrary; it is reserved: checked, but nothing is read or written there.
  */
 #define VG_LOGITS_FP32 0
 #define VG_LOGITS_BF16 1

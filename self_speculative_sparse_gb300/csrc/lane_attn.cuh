@@ -1,8 +1,8 @@
 // The attention kernel of the calls with tall row matrices: shared prefixes (shared_attn.cu) and trees
 // (tree_attn.cu).  A Plan names the call's parameters and finds the runs of a CTA.
 //
-// Attention kernel.  One persistent CTA per SM; the flattened list of steps is split evenly
-// over the CTAs.  A CTA has two "lanes" of eight softmax warps, each with its own 128 rows, S / P
+// Attention kernel.  One persistent CTA per SM; the Plan deals the steps out: the flattened list of them is split evenly
+// over the CTAs, or, for trees with several units a head, pieces of ranges (tasks) go round.  A CTA has two "lanes" of eight softmax warps, each with its own 128 rows, S / P
 // and O in tensor memory; a step is one key tile for both lanes:
 //   pair   the lanes are two row tiles of one KV head and share the step's K and V tile;
 //   heads  the lanes are the same row tile of two KV heads, each with its own K and V tile
@@ -20,7 +20,8 @@
 // then takes sixteen more arrivals: theirs, or at once the producer's.)
 // A tree's runs (Plan::kTree) end inside a key tile, and their last tokens, the nodes, are attended
 // by the bit sets of the rows' nodes.  A run that holds an item's whole key range writes the
-// output itself; partials are two a CTA at most, of its first run and its last.
+// output itself; partials are two a CTA at most: of its first run and its last, or, where tasks go round and
+// ranges are cut, of its two tasks.
 #pragma once
 
 #include "vg_common.cuh"
@@ -202,15 +203,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "[%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
-}
-// a * b + c on two fp32 values at once.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;

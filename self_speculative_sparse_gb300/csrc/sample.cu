@@ -25,11 +25,14 @@
 // alone and finds the cut, and a last pass of the cluster draws.  An interval of too many (flat rows) is cut up
 // again until it is one key, whose ties go by index.
 //
-// What bounds it, at 151936 logits: one row (12 us with top-k 50, 31 with top-p alone), latency: three to seven meetings of
-// the cluster, the passes' loads, of L2 after the first, and code that is fetched once and run once.  Many rows: 393 float
-// ones with top-k 50 take 74 us, 3.2 TB/s: a row's first pass is followed by some 8 us of short steps, which the other
-// resident CTAs' passes cover in part.  393 with top-p alone take 354 us, without any filter 187: the weights' pass is 41
-// instructions a logit, 70 with the intervals; the candidates' pass behind it (6000 of a row of such logits) takes half as long.
+// What bounds it, at 151936 logits: one row (12 us with top-k 50, 31 with top-p alone, call after call in a graph), latency: three
+// to seven meetings of the cluster, the passes' loads, of L2 after the first, and code that is fetched once and run once.  Many
+// rows: 393 float ones with top-k 50 take 75 us, 3.2 TB/s: a row's first pass is followed by some 8 us of short steps, which the
+// other resident CTAs' passes cover in part.  393 with top-p alone take 355 us, without any filter 183 to 187: the weights' pass is
+// 41 instructions a logit, 70 with the intervals; the candidates' pass behind it (6000 of a row of such logits) takes half as long.
+// Two CTAs an SM leave 64 registers a thread; with all paths in one function some 500 bytes of a thread's values are kept in
+// local memory.  Rows that are not whole 16 bytes are read an element at a time: 64 float rows of 151937 logits with top-k 50
+// take 21.8 us, of 151936 14.9; bf16 ones with filtered logits 54.0 and 27.2.
 #include <cooperative_groups.h>
 
 #include "tree_step.h"
@@ -101,14 +104,6 @@ __device__ __forceinline__ Scale make_scale(float top, double c) {
 constexpr float kRoundA = 768.f, kRoundB = 1.5f * 0x1p-6f, kRoundC = 1.5f * 0x1p-20f;  // 1.5 2^23 units
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -1232,23 +1227,23 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int rows) {
         }
       }
     } else {
-    auto mass = [&](float l, int idx) { return x.in(l, idx) ? weight(l, scale, sh.powers) : uint64_t{0}; };
-    Sum part;
-    uint64_t total;
-    x.template each<1>([&](const float (&v)[L], int i) {
+      auto mass = [&](float l, int idx) { return x.in(l, idx) ? weight(l, scale, sh.powers) : uint64_t{0}; };
+      Sum part;
+      uint64_t total;
+      x.template each<1>([&](const float (&v)[L], int i) {
 #pragma unroll
-      for (int e = 0; e < L; e += 2)
-        part.add(parts2(make_float2(v[e], v[e + 1]), scale, sh.powers), x.in(v[e], i + e), x.in(v[e + 1], i + e + 1));
-    });
-    uint64_t sum = part.value();
-    const uint64_t before = sum_before(sum, total), mark = mark_of(total);
-    sum = warp_sum(sum);
-    if (before <= mark && mark < before + sum) {
-      first_past(before, mark, mass, [&](float, int idx, uint64_t y) {
-        p.token[row] = idx;
-        if (p.prob) p.prob[row] = share(y, total);
+        for (int e = 0; e < L; e += 2)
+          part.add(parts2(make_float2(v[e], v[e + 1]), scale, sh.powers), x.in(v[e], i + e), x.in(v[e + 1], i + e + 1));
       });
-    }
+      uint64_t sum = part.value();
+      const uint64_t before = sum_before(sum, total), mark = mark_of(total);
+      sum = warp_sum(sum);
+      if (before <= mark && mark < before + sum) {
+        first_past(before, mark, mass, [&](float, int idx, uint64_t y) {
+          p.token[row] = idx;
+          if (p.prob) p.prob[row] = share(y, total);
+        });
+      }
     }
   } else if (rank == 0 && tid == 0) {
     report(p.status, VG_ERR_DEVICE_BOUNDS);

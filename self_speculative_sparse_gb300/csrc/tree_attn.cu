@@ -28,10 +28,14 @@
 // at the end to the rows that attend it (2 to 3% of the calls of one sequence, less of others).
 //
 // What bounds it: the keys' bytes where a sequence has few row tiles (8 ragged trees of 13 nodes over 4096 to 65536 tokens, with
-// scores: 219 us a call, 5.7 TB/s); the lanes' steps, softmax beside products, where it has many (45 nodes of 8 heads a KV head over
-// 131072 tokens: 178 us, 1.08 PFLOP/s, the tensor pipe active 59% of the kernel); both where each would take about as long (16
-// trees of 64 nodes over 16384 tokens: 217 us, with scores 268 to 279: the warps that multiply the keys with the summed queries
-// are the softmax's).
+// scores: 225 us a call, 5.6 TB/s); the lanes' steps, softmax beside products, where it has many (45 nodes of 8 heads a KV head over
+// 131072 tokens: 175 to 179 us, 1.1 PFLOP/s, the tensor pipe active 55% of the kernel); both where each would take about as long (16
+// trees of 64 nodes over 16384 tokens: 219 us, with scores 271 to 282: the warps that multiply the keys with the summed queries
+// are the softmax's).  What the plan does not do is balance batches of very different lengths that have several units a head: pieces are
+// cut by the longest range, and with more than two units an SM not at all (131072 and 31 times 2048 tokens under 128 nodes each:
+// 1657 us, the floor 216; 24 trees of 80 nodes over 512 to 65536 tokens: 872, 236).  With d = 64 the softmax warps keep some of the row
+// masks' values in local memory (204 to 208 bytes a thread stored, 304 to 332 loaded; none with d = 128), which holds them up: 16
+// trees of 64 nodes over 16384 tokens take 682 us, with d = 128 215.
 #include "lane_attn.cuh"
 #include "tree_bits.h"
 #include "tree_step.h"

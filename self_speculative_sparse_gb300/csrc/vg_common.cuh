@@ -169,6 +169,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// a * b + c on two fp32 values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+
 // ------------------------------------------------------------------ tcgen05 (5th-gen tensor cores)
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand (the layout a TMA
 // box with a 128-byte inner extent and CU_TENSOR_MAP_SWIZZLE_128B produces: rows of
