@@ -1,9 +1,10 @@
 // The attention kernel of the calls with tall row matrices: shared prefixes (shared_attn.cu) and trees
 // (tree_attn.cu).  A Plan names the call's parameters and finds the runs of a CTA.
 //
-// Attention kernel.  One persistent CTA per SM; the Plan deals the steps out: the flattened list of them is split evenly
-// over the CTAs, or, for trees with several units a head, pieces of ranges (tasks) go round.  A CTA has two "lanes" of eight softmax warps, each with its own 128 rows, S / P
-// and O in tensor memory; a step is one key tile for both lanes:
+// Attention kernel.  One persistent CTA per SM; the Plan deals the steps out: the flattened list of them is split
+// evenly over the CTAs, or, for trees with several units a head, pieces of ranges (tasks) go round.  A CTA has two
+// "lanes" of eight softmax warps, each with its own 128 rows, S / P and O in tensor memory; a step is one key tile for
+// both lanes:
 //   pair   the lanes are two row tiles of one KV head and share the step's K and V tile;
 //   heads  the lanes are the same row tile of two KV heads, each with its own K and V tile
 //          (a group's odd last row tile, and every private range).
