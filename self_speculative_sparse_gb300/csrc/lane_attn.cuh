@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
       }
       const bool live = 32 * quad < nrows;  // (a warp without query rows only keeps the barriers' count)
       float mx = neg_inf(), l = 0.f;        // the maximum in use (log2 units), this half's sum
-      bool bare = false;                    // tree: a row of these warps has attended nothing yet
+      bool bare = false;                    // tree: a row of these warps has perhaps nothing that weighs anything yet
       for (int n = 0; n <= last; ++n) {
         const int left = keys - n * KT;  // keys of the tile (128 or more: all)
         // S is awaited, and in the meantime the keys are scored (a pair's two lanes share the tile).  A run's first
@@ -808,10 +808,10 @@ __global__ void __launch_bounds__(SCfg<D>::THREADS, 1)
           tc_st1(to_mine, t);
           tc_wait_st();
           tc_fence_before();
-          named_bar_or(pair_bar, 64, false);
+          // (bare: of a half, which a row's other half may make up for; the next tile settles it)
+          bare = named_bar_or(pair_bar, 64, TREE && row < nrows && t == neg_inf()) && TREE;
           tc_fence_after();
           mx = fmaxf(t, tc_ld1_sync(to_other));
-          if (TREE && nodes) bare = named_bar_or(pair_bar, 64, row < nrows && mx == neg_inf());
         } else if (TREE && bare) {
           // (O is in use: each thread reads its row's whole tile.  What such a row has of O is 0)
           const float t = row_max(left, tok, nodes);
